@@ -75,7 +75,8 @@ typedef enum tp_status {
   TP_ERR_WORKSPACE = 8     /* ws is NULL or smaller than tp_workspace_size()     */
 } tp_status;
 
-typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1 } tp_dtype;
+/* TP_F16 is taken by the query/key norm + rotary and window attention calls. */
+typedef enum tp_dtype { TP_F32 = 0, TP_BF16 = 1, TP_F16 = 2 } tp_dtype;
 
 typedef enum tp_op {
   TP_OP_MLP_FWD = 0,
@@ -86,7 +87,8 @@ typedef enum tp_op {
   TP_OP_BLOCK_FWD = 5,
   TP_OP_BLOCK_BWD = 6,
   TP_OP_VOCAB_CE_FWD = 7,   /* f is the vocabulary size V */
-  TP_OP_VOCAB_EMBED_BWD = 8 /* depends on M only */
+  TP_OP_VOCAB_EMBED_BWD = 8, /* depends on M only */
+  TP_OP_QK_NORM_ROPE_BWD = 9 /* h is the head dimension d; depends on d only */
 } tp_op;
 
 /*
@@ -391,6 +393,54 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
                           const void* logits, const float* lse, const float* dloss,
                           void* dlogits, void* dX, void* dE, int64_t M, int64_t h, int64_t V,
                           int t, tp_dtype dtype, void* stream);
+
+/*
+ * RMS norm of every query and key head with the rotary position in the same
+ * pass.  For a head's row x of d values with weight g (gq or gk, shared by
+ * the heads) and the token's position p:
+ *   z = x / sqrt(mean(x^2) + eps) * g      (norm == 0: z = x, g is not read)
+ *   (y_a, y_b) = (z_a cos t - z_b sin t, z_b cos t + z_a sin t),
+ *   t = p * inv_freq[i], over the pairs (a, b) = (i, i + d_rot / 2), or
+ *   (2 i, 2 i + 1) with interleaved != 0, i < d_rot / 2; the values from
+ *   d_rot on are normalised and not rotated.
+ * Statistics and rotation in fp32, the angles reduced in fp64 (any int32
+ * position); one rounding to dtype at the end.
+ *   Q [M, heads * d], K [M, kv_heads * d] with row strides ldq, ldk
+ *   (elements): columns of a wider projection output may be given in place.
+ *   Qo, Ko likewise with ldqo, ldko; Qo may be Q and Ko may be K (serving),
+ *   no other overlap is allowed.  K and Ko may be NULL when kv_heads == 0.
+ *   gq, gk [d] dtype or NULL (1).  pos [M] int32 and inv_freq [d_rot / 2]
+ *   fp64 on the device; both may be NULL when d_rot == 0.
+ *   dtype TP_BF16, TP_F16 or TP_F32.  d % 8 == 0, 8 <= d <= 256,
+ *   d_rot % 16 == 0, 0 <= d_rot <= d; M == 0 is a no-op.
+ * Errors: NULL; sizes; d_rot or strides out of range (TP_ERR_SHAPE);
+ *   alignment (strides and d multiples of 8 elements, d_rot of 16, 16-byte
+ *   pointers); d > 256 is TP_ERR_UNSUPPORTED; dtype.
+ */
+tp_status tp_qk_norm_rope_fwd(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                              const void* gq, const void* gk, const int32_t* pos,
+                              const double* inv_freq, void* Qo, int64_t ldqo, void* Ko,
+                              int64_t ldko, int64_t M, int heads, int kv_heads, int d, int d_rot,
+                              int norm, int interleaved, float eps, tp_dtype dtype, void* stream);
+
+/*
+ * Backward of tp_qk_norm_rope_fwd: with dz the gradient dy rotated by -t and
+ * r = 1 / sqrt(mean(x^2) + eps) (recomputed from the forward's INPUT x),
+ *   dx = r dz g - x r^3 mean(dz g x),   dg = sum over tokens and heads of dz x r.
+ *   dQo, dKo: gradients of Qo, Ko; dQ, dK receive dx (dQ may be dQo, dK may be
+ *   dKo); each with its row stride.  dgq, dgk [d] dtype, each skipped when
+ *   NULL (and when norm == 0).  Deterministic (fixed order of every sum).
+ *   ws: tp_workspace_size(TP_OP_QK_NORM_ROPE_BWD, M, d, 0, 0, 1, dtype); may
+ *   be NULL when neither dgq nor dgk is asked for.
+ * Errors: as the forward, plus TP_ERR_WORKSPACE.  M == 0 writes zero dgq, dgk.
+ */
+tp_status tp_qk_norm_rope_bwd(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                              const void* gq, const void* gk, const int32_t* pos,
+                              const double* inv_freq, const void* dQo, int64_t lddqo,
+                              const void* dKo, int64_t lddko, void* dQ, int64_t lddq, void* dK,
+                              int64_t lddk, void* dgq, void* dgk, int64_t M, int heads,
+                              int kv_heads, int d, int d_rot, int norm, int interleaved, float eps,
+                              tp_dtype dtype, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Workspace bytes that `op` needs for these sizes (M = b*s tokens; f is

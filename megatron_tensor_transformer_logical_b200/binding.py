@@ -19,10 +19,10 @@ LIB_PATH = os.path.join(_HERE, "libtp.so")
 
 TP_OK, TP_ERR_NULL, TP_ERR_SHAPE, TP_ERR_ALIGN, TP_ERR_DTYPE = 0, 1, 2, 3, 4
 TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_KERNEL, TP_ERR_WORKSPACE = 5, 6, 7, 8
-TP_F32, TP_BF16 = 0, 1
+TP_F32, TP_BF16, TP_F16 = 0, 1, 2
 TP_OP_MLP_FWD, TP_OP_MLP_BWD, TP_OP_ATTN_FWD, TP_OP_ATTN_BWD = 0, 1, 2, 3
 TP_OP_LN_BWD, TP_OP_BLOCK_FWD, TP_OP_BLOCK_BWD, TP_OP_VOCAB_CE_FWD = 4, 5, 6, 7
-TP_OP_VOCAB_EMBED_BWD = 8
+TP_OP_VOCAB_EMBED_BWD, TP_OP_QK_NORM_ROPE_BWD = 8, 9
 
 (TP_KIND_GEMM_TCGEN05, TP_KIND_GEMM_SIMT, TP_KIND_ATTN_FWD, TP_KIND_ATTN_BWD, TP_KIND_REDUCE,
  TP_KIND_VOCAB) = range(6)
@@ -36,7 +36,7 @@ EXPORTS = ("tp_linear_col", "tp_linear_row", "tp_mlp_fwd", "tp_mlp_bwd", "tp_att
            "tp_mlp_fwd_noalloc", "tp_profile_count", "tp_profile_record", "tp_layernorm_fwd",
            "tp_layernorm_bwd", "tp_block_fwd", "tp_block_bwd", "tp_vocab_embed_fwd",
            "tp_vocab_embed_bwd", "tp_vocab_ce_fwd", "tp_vocab_ce_bwd", "tp_gemm_plan",
-           "tp_selftest_bounded_wait")
+           "tp_selftest_bounded_wait", "tp_qk_norm_rope_fwd", "tp_qk_norm_rope_bwd")
 
 _W_FIELDS = ("ln1_g", "ln1_b", "Wqkv", "Wo", "ln2_g", "ln2_b", "A", "bA", "B", "bB")
 _S_FIELDS = ("Xn1", "mean1", "rstd1", "QKV", "O", "LSE", "X1", "Xn2", "mean2", "rstd2", "Y")
@@ -113,6 +113,11 @@ def load() -> ctypes.CDLL:
     L.tp_vocab_ce_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, vp, sz, vp]
     L.tp_vocab_ce_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
                                   vp]
+    L.tp_qk_norm_rope_fwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, i64, i32,
+                                      i32, i32, i32, i32, i32, f32, i32, vp]
+    L.tp_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64,
+                                      vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, i32, f32, i32,
+                                      vp, sz, vp]
     L.tp_workspace_size.argtypes = [i32, i64, i64, i64, i32, i32, i32]
     L.tp_workspace_size.restype = sz
     L.tp_last_error.argtypes = []
@@ -300,6 +305,111 @@ def tp_vocab_ce_bwd(X, E, targets, logits, lse, dloss, dlogits, dX, dE, t: int,
     _check(load().tp_vocab_ce_bwd(_ptr(X), _ptr(E), _ids(targets), _ptr(logits), _ptr(lse),
                                   _ptr(dloss), _ptr(dlogits), _ptr(dX), _ptr(dE), M, h, V, t,
                                   _dtype(X), _stream(stream)))
+
+
+_DTYPES = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float16: TP_F16}
+
+
+def _rows(t: Optional[torch.Tensor], like: torch.Tensor, what: str):
+    """(pointer, row stride) of a 2-D tensor whose rows are dense."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D tensor with dense rows is required")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what}: dtype or device differs from the first tensor's")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _side(t: Optional[torch.Tensor], n: int, dtype, like: torch.Tensor, what: str):
+    """Pointer of a dense 1-D side tensor of n elements (or None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != like.device:
+        raise ValueError(f"{what}: {n} elements of {dtype} on {like.device} are required")
+    return _ptr(t)
+
+
+class _on:
+    """Makes the tensors' device current for the call and yields its stream
+    (the given one, else the device's current stream)."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not t.is_cuda:
+            raise ValueError("libtp takes CUDA tensors")
+        self.dev, self.stream, self.prev = t.device.index, stream, -1
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        if cur != self.dev:
+            self.prev = cur
+            torch.cuda.set_device(self.dev)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.prev >= 0:
+            torch.cuda.set_device(self.prev)
+
+
+def _same_shape(t: Optional[torch.Tensor], like: Optional[torch.Tensor], what: str) -> None:
+    if t is not None and (like is None or t.shape != like.shape):
+        raise ValueError(f"{what}: wrong shape {tuple(t.shape)}")
+
+
+def _qk_sizes(Q, K, gq, gk, pos, inv_freq, d: int):
+    M, nq = Q.shape
+    nk = 0 if K is None else K.shape[1]
+    if Q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {Q.dtype}")
+    if d <= 0 or nq % d or nk % d or (K is not None and K.shape[0] != M):
+        raise ValueError("Q [M, heads * d] and K [M, kv_heads * d] are required")
+    d_rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return (M, nq // d, nk // d, d_rot, _side(gq, d, Q.dtype, Q, "gq"),
+            _side(gk, d, Q.dtype, Q, "gk"), _side(pos, M, torch.int32, Q, "pos"),
+            _side(inv_freq, d_rot // 2, torch.float64, Q, "inv_freq"))
+
+
+def tp_qk_norm_rope_fwd(Q, K, gq, gk, pos, inv_freq, Qo, Ko, d: int, norm: bool = True,
+                        interleaved: bool = False, eps: float = 1e-6, stream=None) -> None:
+    """Qo, Ko = rotary(RMSNorm(Q, K)) per head of d columns; Q [M, heads * d], K
+    [M, kv_heads * d] (row-strided views allowed, K may be None), pos int32 [M],
+    inv_freq fp64 [d_rot / 2] (None: no rotation).  Qo may be Q, Ko may be K."""
+    M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq, d)
+    _same_shape(Qo, Q, "Qo")
+    _same_shape(Ko, K, "Ko")
+    (q, ldq), (k, ldk) = _rows(Q, Q, "Q"), _rows(K, Q, "K")
+    (qo, ldqo), (ko, ldko) = _rows(Qo, Q, "Qo"), _rows(Ko, Q, "Ko")
+    with _on(Q, stream) as st:
+        _check(load().tp_qk_norm_rope_fwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, qo, ldqo, ko, ldko,
+                                          M, heads, kv, d, d_rot, int(norm), int(interleaved), eps,
+                                          _DTYPES[Q.dtype], st))
+
+
+def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk, d: int, ws,
+                        norm: bool = True, interleaved: bool = False, eps: float = 1e-6,
+                        stream=None) -> None:
+    """Backward of tp_qk_norm_rope_fwd from its inputs Q, K and the gradients dQo,
+    dKo of its outputs; dQ may be dQo, dK may be dKo; dgq, dgk may be None."""
+    M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq, d)
+    for t, n in ((dQo, "dQo"), (dQ, "dQ")):
+        _same_shape(t, Q, n)
+    for t, n in ((dKo, "dKo"), (dK, "dK")):
+        _same_shape(t, K, n)
+    (q, ldq), (k, ldk) = _rows(Q, Q, "Q"), _rows(K, Q, "K")
+    (gqo, lgqo), (gko, lgko) = _rows(dQo, Q, "dQo"), _rows(dKo, Q, "dKo")
+    (dq, lddq), (dk, lddk) = _rows(dQ, Q, "dQ"), _rows(dK, Q, "dK")
+    with _on(Q, stream) as st:
+        _check(load().tp_qk_norm_rope_bwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, gqo, lgqo, gko, lgko,
+                                          dq, lddq, dk, lddk, _side(dgq, d, Q.dtype, Q, "dgq"),
+                                          _side(dgk, d, Q.dtype, Q, "dgk"), M, heads, kv, d, d_rot,
+                                          int(norm), int(interleaved), eps, _DTYPES[Q.dtype],
+                                          _ptr(ws), 0 if ws is None else ws.numel() *
+                                          ws.element_size(), st))
+
+
+def qk_norm_rope_workspace(M: int, d: int, device="cuda") -> torch.Tensor:
+    """Workspace of tp_qk_norm_rope_bwd."""
+    return workspace(TP_OP_QK_NORM_ROPE_BWD, M, d, 0, 0, 1, TP_BF16, device)
 
 
 def tp_device_status(stream=None) -> None:

@@ -891,6 +891,59 @@ tp_status vocab_ce_bwd(const void* X, const void* E, const int32_t* targets, con
   return TP_OK;
 }
 
+// ------------------------------------------- query / key norm + rotary
+
+tp_status check_half_dtype(tp_dtype d) {
+  if (d != TP_BF16 && d != TP_F16) return fail(TP_ERR_DTYPE, "dtype must be bf16 or fp16");
+  return TP_OK;
+}
+
+// Row stride `ld` of a matrix of `cols` columns (elements).
+tp_status check_ld(int64_t ld, int64_t cols) {
+  if (ld < cols) return fail(TP_ERR_SHAPE, "row stride smaller than the row");
+  if (ld % 8 != 0) return fail(TP_ERR_ALIGN, "row stride not a multiple of 8 elements");
+  if (ld > kMaxDim) return fail(TP_ERR_SHAPE, "row stride too large");
+  return TP_OK;
+}
+
+size_t qk_rope_bwd_ws(int64_t d) { return align_up(qk_rope_bwd_scratch_bytes(d), 256); }
+
+tp_status qk_rope(const QkRope& r, bool bwd, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (r.dtype != TP_F16) TP_TRY(check_dtype(r.dtype));
+  if (r.M < 0 || r.heads <= 0 || r.kv_heads < 0 || r.d <= 0)
+    return fail(TP_ERR_SHAPE, "M and kv_heads must be >= 0, heads and d positive");
+  if (r.d % 8 != 0) return fail(TP_ERR_ALIGN, "d must be a multiple of 8");
+  if (r.d > 256) return fail(TP_ERR_UNSUPPORTED, "d must be at most 256");
+  if (r.d_rot < 0 || r.d_rot > r.d) return fail(TP_ERR_SHAPE, "d_rot must be in [0, d]");
+  if (r.d_rot % 16 != 0) return fail(TP_ERR_ALIGN, "d_rot must be a multiple of 16");
+  const int64_t nq = int64_t(r.heads) * r.d, nk = int64_t(r.kv_heads) * r.d;
+  if (!dims_ok({r.M, nq, nk})) return fail(TP_ERR_SHAPE, "sizes must be below 2^31 - 256");
+  const void* qout = bwd ? r.dq : r.qo;
+  const void* kout = bwd ? r.dk : r.ko;
+  if (r.M > 0) {
+    if (!r.q || !qout || (bwd && !r.dqo)) return fail(TP_ERR_NULL, "the query tensors are required");
+    if (r.kv_heads > 0 && (!r.k || !kout || (bwd && !r.dko)))
+      return fail(TP_ERR_NULL, "the key tensors are required when kv_heads > 0");
+    if (r.d_rot > 0 && (!r.pos || !r.inv_freq))
+      return fail(TP_ERR_NULL, "pos and inv_freq are required when d_rot > 0");
+    TP_TRY(check_ld(r.ldq, nq));
+    TP_TRY(check_ld(bwd ? r.lddq : r.ldqo, nq));
+    if (bwd) TP_TRY(check_ld(r.lddqo, nq));
+    if (r.kv_heads > 0) {
+      TP_TRY(check_ld(r.ldk, nk));
+      TP_TRY(check_ld(bwd ? r.lddk : r.ldko, nk));
+      if (bwd) TP_TRY(check_ld(r.lddko, nk));
+    }
+  }
+  TP_TRY(check_ptrs_aligned({r.q, r.k, r.gq, r.gk, qout, kout, r.dqo, r.dko, r.dgq, r.dgk, ws}));
+  if ((reinterpret_cast<uintptr_t>(r.inv_freq) & 7u) || (reinterpret_cast<uintptr_t>(r.pos) & 3u))
+    return fail(TP_ERR_ALIGN, "pos or inv_freq not aligned to its elements");
+  const bool want_dg = bwd && r.norm && (r.dgq || r.dgk);
+  if (want_dg && r.M > 0 && (ws == nullptr || ws_bytes < qk_rope_bwd_ws(r.d)))
+    return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_workspace_size()");
+  return launch_qk_rope(r, bwd, ws, stream);
+}
+
 }  // namespace
 }  // namespace tp
 
@@ -1042,9 +1095,40 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
                                dtype, static_cast<cudaStream_t>(stream));)
 }
 
+tp_status tp_qk_norm_rope_fwd(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                              const void* gq, const void* gk, const int32_t* pos,
+                              const double* inv_freq, void* Qo, int64_t ldqo, void* Ko,
+                              int64_t ldko, int64_t M, int heads, int kv_heads, int d, int d_rot,
+                              int norm, int interleaved, float eps, tp_dtype dtype,
+                              void* stream) {
+  TP_GUARD(QkRope r; r.q = Q; r.ldq = ldq; r.k = K; r.ldk = ldk; r.gq = gq; r.gk = gk; r.pos = pos;
+           r.inv_freq = inv_freq; r.qo = Qo; r.ldqo = ldqo; r.ko = Ko; r.ldko = ldko; r.M = M;
+           r.heads = heads; r.kv_heads = kv_heads; r.d = d; r.d_rot = d_rot; r.norm = norm;
+           r.interleaved = interleaved; r.eps = eps; r.dtype = dtype;
+           return qk_rope(r, false, nullptr, 0, static_cast<cudaStream_t>(stream));)
+}
+
+tp_status tp_qk_norm_rope_bwd(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                              const void* gq, const void* gk, const int32_t* pos,
+                              const double* inv_freq, const void* dQo, int64_t lddqo,
+                              const void* dKo, int64_t lddko, void* dQ, int64_t lddq, void* dK,
+                              int64_t lddk, void* dgq, void* dgk, int64_t M, int heads,
+                              int kv_heads, int d, int d_rot, int norm, int interleaved, float eps,
+                              tp_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  TP_GUARD(QkRope r; r.q = Q; r.ldq = ldq; r.k = K; r.ldk = ldk; r.gq = gq; r.gk = gk; r.pos = pos;
+           r.inv_freq = inv_freq; r.dqo = dQo; r.lddqo = lddqo; r.dko = dKo; r.lddko = lddko;
+           r.dq = dQ; r.lddq = lddq; r.dk = dK; r.lddk = lddk; r.dgq = dgq; r.dgk = dgk; r.M = M;
+           r.heads = heads; r.kv_heads = kv_heads; r.d = d; r.d_rot = d_rot; r.norm = norm;
+           r.interleaved = interleaved; r.eps = eps; r.dtype = dtype;
+           return qk_rope(r, true, ws, ws_bytes, static_cast<cudaStream_t>(stream));)
+}
+
 size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, int t,
                          tp_dtype dtype) {
   try {
+    if (op == TP_OP_QK_NORM_ROPE_BWD)  // also fp16
+      return (M > 0 && h > 0 && h <= 256 && dtype >= TP_F32 && dtype <= TP_F16) ? qk_rope_bwd_ws(h)
+                                                                               : 0;
     if (M <= 0 || h <= 0 || t < 1 || (dtype != TP_F32 && dtype != TP_BF16)) return 0;
     if (!dims_ok({M, h, f})) return 0;
     switch (op) {
@@ -1057,6 +1141,7 @@ size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, i
       case TP_OP_BLOCK_BWD: return (heads > 0 && f > 0) ? block_bwd_ws(M, h, f, heads) : 0;
       case TP_OP_VOCAB_CE_FWD: return (f > 0 && f % t == 0) ? ce_fwd_ws(M, f, t) : 0;
       case TP_OP_VOCAB_EMBED_BWD: return embed_bwd_ws(M);
+      case TP_OP_QK_NORM_ROPE_BWD: break;  // answered above
     }
   } catch (...) {
   }

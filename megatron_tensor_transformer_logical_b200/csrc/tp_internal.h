@@ -193,6 +193,24 @@ tp_status launch_ce_dlogits(const void* logits, const float* lse, const int* tar
                             const float* dloss, void* dlogits, int64_t M, int64_t V,
                             cudaStream_t stream);
 
+// Query / key norm with rotary positions (tp_qk_norm_rope_fwd / _bwd).
+struct QkRope {
+  const void *q = nullptr, *k = nullptr, *gq = nullptr, *gk = nullptr;
+  const int* pos = nullptr;
+  const double* inv_freq = nullptr;
+  void *qo = nullptr, *ko = nullptr;                   // forward
+  const void *dqo = nullptr, *dko = nullptr;           // backward
+  void *dq = nullptr, *dk = nullptr, *dgq = nullptr, *dgk = nullptr;
+  int64_t ldq = 0, ldk = 0, ldqo = 0, ldko = 0, lddqo = 0, lddko = 0, lddq = 0, lddk = 0;
+  int64_t M = 0;
+  int heads = 0, kv_heads = 0, d = 0, d_rot = 0, norm = 1, interleaved = 0;
+  float eps = 0.0f;
+  tp_dtype dtype = TP_BF16;
+};
+// Partial weight gradients, one row of 2 d floats per block.
+size_t qk_rope_bwd_scratch_bytes(int64_t d);
+tp_status launch_qk_rope(const QkRope& r, bool bwd, void* scratch, cudaStream_t stream);
+
 // Attention core (per head causal softmax attention), bf16 with d = 128.
 struct AttnShape {
   int64_t b = 0, s = 0, h = 0;
