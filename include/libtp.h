@@ -443,6 +443,81 @@ tp_status tp_qk_norm_rope_bwd(const void* Q, int64_t ldq, const void* K, int64_t
                               tp_dtype dtype, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * Attention over a sliding window with sinks, on projected (and rotated)
+ * heads.  Query r of a sequence sits at position p = r + sk - sq and sees key
+ * c when c <= p and (p - c < window or c < sinks): itself, the window - 1
+ * keys before it and the first `sinks` keys.  Per head
+ *   O = softmax(scale Q K^T over the visible keys) V;
+ * query head j reads key / value head j / (heads / kv_heads).
+ * window >= sk is full causal attention.  With sq > sk the first sq - sk
+ * queries see nothing: their O is 0 and their LSE -inf, and they get and pass
+ * no gradient.
+ *   Q [b * sq, heads * d], K, V [b * sk, kv_heads * d], O as Q; each with its
+ *   row stride in elements (columns of a wider matrix may be given; a
+ *   sequence's rows follow one another).  O overlaps no input.
+ *   LSE [b, heads, sq] fp32: natural-log softmax denominators.
+ *   scale 0 stands for 1 / sqrt(d).  dtype TP_BF16 or TP_F16 for all
+ *   matrices; d 64 or 128.  P is rounded to dtype for P V, sums and statistics
+ *   are fp32.
+ * What a query does not see is multiplied by a probability of zero inside its
+ * tile, so every K and V value of its own sequence must be finite; other
+ * sequences never enter.
+ * Errors: NULL; sizes, heads % kv_heads, strides (TP_ERR_SHAPE); window < 1,
+ *   sinks < 0, scale < 0 or not finite (TP_ERR_SHAPE); alignment; dtype; d
+ *   other than 64 or 128 (TP_ERR_UNSUPPORTED).
+ */
+tp_status tp_window_attn_fwd(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, void* O, int64_t ldo, float* LSE, int64_t b, int64_t sq,
+                             int64_t sk, int heads, int kv_heads, int d, int64_t window,
+                             int64_t sinks, float scale, tp_dtype dtype, void* stream);
+
+/*
+ * Backward of tp_window_attn_fwd: with P the probabilities (recomputed from
+ * LSE), D = rowsum(dO * O) and dS = P (dO V^T - D),
+ *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+ * dK and dV summed over the query heads that share them.  Every row of dQ,
+ * dK and dV is written (zeros where nothing is seen).  Deterministic.
+ *   O, LSE: from the forward, same arguments.  No output overlaps an input.
+ *   ws: tp_window_attn_workspace_size() bytes.
+ * Errors: as the forward, plus TP_ERR_WORKSPACE.
+ */
+tp_status tp_window_attn_bwd(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, const void* O, int64_t ldo, const float* LSE,
+                             const void* dO, int64_t lddo, void* dQ, int64_t lddq, void* dK,
+                             int64_t lddk, void* dV, int64_t lddv, int64_t b, int64_t sq,
+                             int64_t sk, int heads, int kv_heads, int d, int64_t window,
+                             int64_t sinks, float scale, tp_dtype dtype, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* Workspace bytes of tp_window_attn_bwd (row terms, and fp32 partials of the
+ * key tiles it cuts); 0 for invalid arguments. */
+size_t tp_window_attn_workspace_size(int64_t b, int64_t sq, int64_t sk, int heads, int kv_heads,
+                                     int d, int64_t window, int64_t sinks);
+
+/*
+ * The same attention for one new token per sequence over a cache: sequence i
+ * has lens[i] keys (the new token's included) and its query sits at position
+ * lens[i] - 1.
+ *   Q, O [b, heads * d] with row strides; K, V: sequence i's key c, head g at
+ *   i * batch stride + c * row stride + g * d (elements), c < cap.
+ *   lens [b] int32 on the device (values outside [0, cap] are clamped to it);
+ *   lens[i] == 0: O 0, LSE -inf.  Keys at and past lens[i] are not read.
+ *   LSE [b, heads] fp32 or NULL.
+ *   ws: tp_window_decode_workspace_size() bytes.
+ * Errors: as tp_window_attn_fwd, plus TP_ERR_WORKSPACE.
+ */
+tp_status tp_window_attn_decode(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                                int64_t batch_k, const void* V, int64_t ldv, int64_t batch_v,
+                                const int32_t* lens, void* O, int64_t ldo, float* LSE, int64_t b,
+                                int64_t cap, int heads, int kv_heads, int d, int64_t window,
+                                int64_t sinks, float scale, tp_dtype dtype, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Workspace bytes of tp_window_attn_decode; 0 for invalid arguments. */
+size_t tp_window_decode_workspace_size(int64_t b, int64_t cap, int heads, int kv_heads, int d,
+                                       int64_t window, int64_t sinks);
+
+/*
  * Workspace bytes that `op` needs for these sizes (M = b*s tokens; f is
  * ignored by the attention and LayerNorm ops, heads by the MLP and LayerNorm
  * ops).  Returns 0 for invalid arguments.  The size covers the worst case

@@ -36,7 +36,9 @@ EXPORTS = ("tp_linear_col", "tp_linear_row", "tp_mlp_fwd", "tp_mlp_bwd", "tp_att
            "tp_mlp_fwd_noalloc", "tp_profile_count", "tp_profile_record", "tp_layernorm_fwd",
            "tp_layernorm_bwd", "tp_block_fwd", "tp_block_bwd", "tp_vocab_embed_fwd",
            "tp_vocab_embed_bwd", "tp_vocab_ce_fwd", "tp_vocab_ce_bwd", "tp_gemm_plan",
-           "tp_selftest_bounded_wait", "tp_qk_norm_rope_fwd", "tp_qk_norm_rope_bwd")
+           "tp_selftest_bounded_wait", "tp_qk_norm_rope_fwd", "tp_qk_norm_rope_bwd",
+           "tp_window_attn_fwd", "tp_window_attn_bwd", "tp_window_attn_workspace_size",
+           "tp_window_attn_decode", "tp_window_decode_workspace_size")
 
 _W_FIELDS = ("ln1_g", "ln1_b", "Wqkv", "Wo", "ln2_g", "ln2_b", "A", "bA", "B", "bB")
 _S_FIELDS = ("Xn1", "mean1", "rstd1", "QKV", "O", "LSE", "X1", "Xn2", "mean2", "rstd2", "Y")
@@ -118,8 +120,16 @@ def load() -> ctypes.CDLL:
     L.tp_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64,
                                       vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, i32, f32, i32,
                                       vp, sz, vp]
+    L.tp_window_attn_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32,
+                                     i32, i32, i64, i64, f32, i32, vp]
+    L.tp_window_attn_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp,
+                                     i64, vp, i64, i64, i64, i64, i32, i32, i32, i64, i64, f32,
+                                     i32, vp, sz, vp]
+    L.tp_window_attn_decode.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, vp, i64,
+                                        i64, i32, i32, i32, i64, i64, f32, i32, vp, sz, vp]
+    L.tp_window_attn_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32, i64, i64]
+    L.tp_window_decode_workspace_size.argtypes = [i64, i64, i32, i32, i32, i64, i64]
     L.tp_workspace_size.argtypes = [i32, i64, i64, i64, i32, i32, i32]
-    L.tp_workspace_size.restype = sz
     L.tp_last_error.argtypes = []
     L.tp_last_error.restype = ctypes.c_char_p
     L.tp_device_status.argtypes = [vp]
@@ -133,8 +143,10 @@ def load() -> ctypes.CDLL:
     L.tp_profile_record.argtypes = [ctypes.c_int64, ctypes.POINTER(LaunchRecord)]
     L.tp_gemm_plan.argtypes = [i64, i64, i64, i64, i32, i32, i32, ctypes.POINTER(GemmUnit), i64]
     for name in EXPORTS:
-        if name not in ("tp_workspace_size", "tp_last_error", "tp_launch_count",
-                        "tp_profile_count", "tp_gemm_plan"):
+        if name.endswith("_workspace_size"):
+            getattr(L, name).restype = sz
+        elif name not in ("tp_last_error", "tp_launch_count", "tp_profile_count",
+                          "tp_gemm_plan"):
             getattr(L, name).restype = ctypes.c_int
     L.tp_launch_count.restype = ctypes.c_int64
     L.tp_gemm_plan.restype = ctypes.c_int64
@@ -410,6 +422,108 @@ def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk,
 def qk_norm_rope_workspace(M: int, d: int, device="cuda") -> torch.Tensor:
     """Workspace of tp_qk_norm_rope_bwd."""
     return workspace(TP_OP_QK_NORM_ROPE_BWD, M, d, 0, 0, 1, TP_BF16, device)
+
+
+def _heads(x, n: int, what: str) -> int:
+    """Head dimension of [.., n * d] columns."""
+    if n <= 0 or x.shape[-1] % n:
+        raise ValueError(f"{what}: {x.shape[-1]} columns do not hold {n} heads")
+    return x.shape[-1] // n
+
+
+def _window_sizes(Q, K, V, b: int, heads: int, kv_heads: int):
+    if Q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {Q.dtype}")
+    d = _heads(Q, heads, "Q")
+    if b <= 0 or Q.shape[0] % b or K.shape[0] % b or K.shape[1] != kv_heads * d:
+        raise ValueError("Q [b * sq, heads * d] and K [b * sk, kv_heads * d] are required")
+    _same_shape(V, K, "V")
+    return Q.shape[0] // b, K.shape[0] // b, d
+
+
+def tp_window_attn_fwd(Q, K, V, O, LSE, b: int, heads: int, kv_heads: int, window: int,
+                       sinks: int = 0, scale: float = 0.0, stream=None) -> None:
+    """O = softmax attention of Q [b * sq, heads * d] over K, V [b * sk, kv_heads *
+    d] (row-strided views allowed): each query sees itself, the window - 1 keys
+    before it and the first `sinks` keys.  LSE fp32 [b, heads, sq]; scale 0: 1 /
+    sqrt(d)."""
+    sq, sk, d = _window_sizes(Q, K, V, b, heads, kv_heads)
+    _same_shape(O, Q, "O")
+    (q, ldq), (k, ldk), (v, ldv), (o, ldo) = (_rows(Q, Q, "Q"), _rows(K, Q, "K"),
+                                              _rows(V, Q, "V"), _rows(O, Q, "O"))
+    lse = _side(LSE, b * heads * sq, torch.float32, Q, "LSE")
+    with _on(Q, stream) as st:
+        _check(load().tp_window_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, b, sq, sk, heads,
+                                         kv_heads, d, window, sinks, scale, _DTYPES[Q.dtype], st))
+
+
+def tp_window_attn_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, b: int, heads: int, kv_heads: int,
+                       window: int, sinks: int, ws, scale: float = 0.0, stream=None) -> None:
+    """Backward of tp_window_attn_fwd; ws from window_attn_workspace()."""
+    sq, sk, d = _window_sizes(Q, K, V, b, heads, kv_heads)
+    for t, n in ((O, "O"), (dO, "dO"), (dQ, "dQ")):
+        _same_shape(t, Q, n)
+    for t, n in ((dK, "dK"), (dV, "dV")):
+        _same_shape(t, K, n)
+    (q, ldq), (k, ldk), (v, ldv), (o, ldo) = (_rows(Q, Q, "Q"), _rows(K, Q, "K"),
+                                              _rows(V, Q, "V"), _rows(O, Q, "O"))
+    (go, lgo), (gq, lgq), (gk, lgk), (gv, lgv) = (_rows(dO, Q, "dO"), _rows(dQ, Q, "dQ"),
+                                                  _rows(dK, Q, "dK"), _rows(dV, Q, "dV"))
+    lse = _side(LSE, b * heads * sq, torch.float32, Q, "LSE")
+    with _on(Q, stream) as st:
+        _check(load().tp_window_attn_bwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, go, lgo, gq, lgq, gk,
+                                         lgk, gv, lgv, b, sq, sk, heads, kv_heads, d, window,
+                                         sinks, scale, _DTYPES[Q.dtype], _ptr(ws),
+                                         ws.numel() * ws.element_size(), st))
+
+
+def tp_window_attn_decode(Q, K, V, lens, O, LSE, heads: int, kv_heads: int, window: int,
+                          sinks: int, ws, scale: float = 0.0, stream=None) -> None:
+    """One token per sequence over a cache: Q, O [b, heads * d], K, V [b, cap,
+    kv_heads * d] (strided views allowed), lens int32 [b] on the device (keys per
+    sequence, the new token's included), LSE fp32 [b, heads] or None."""
+    if Q.dtype not in _DTYPES:
+        raise ValueError(f"unsupported dtype {Q.dtype}")
+    b, d = Q.shape[0], _heads(Q, heads, "Q")
+    if K.dim() != 3 or K.shape[0] != b or K.shape[2] != kv_heads * d or K.stride(2) != 1 \
+            or V.stride(2) != 1:
+        raise ValueError("K, V [b, cap, kv_heads * d] with dense rows are required")
+    _same_shape(O, Q, "O")
+    _same_shape(V, K, "V")
+    for t, n in ((K, "K"), (V, "V")):
+        if t.dtype != Q.dtype or t.device != Q.device:
+            raise ValueError(f"{n}: dtype or device differs from the first tensor's")
+    cap = K.shape[1]
+    (q, ldq), (o, ldo) = _rows(Q, Q, "Q"), _rows(O, Q, "O")
+    ldk, ldv = (t.stride(1) if cap > 1 else t.shape[2] for t in (K, V))
+    bsk, bsv = (t.stride(0) if b > 1 else 0 for t in (K, V))
+    plens = _side(lens, b, torch.int32, Q, "lens")
+    lse = _side(LSE, b * heads, torch.float32, Q, "LSE")
+    with _on(Q, stream) as st:
+        _check(load().tp_window_attn_decode(q, ldq, K.data_ptr(), ldk, bsk, V.data_ptr(), ldv, bsv,
+                                            plens, o, ldo, lse, b, cap, heads, kv_heads, d, window,
+                                            sinks, scale, _DTYPES[Q.dtype], _ptr(ws),
+                                            ws.numel() * ws.element_size(), st))
+
+
+def _bytes(n: int, device) -> torch.Tensor:
+    if n == 0:
+        raise TPError(TP_ERR_SHAPE, "invalid sizes for the workspace query")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def window_attn_workspace(b: int, sq: int, sk: int, heads: int, kv_heads: int, d: int, window: int,
+                          sinks: int = 0, device="cuda") -> torch.Tensor:
+    """Workspace of tp_window_attn_bwd."""
+    return _bytes(load().tp_window_attn_workspace_size(b, sq, sk, heads, kv_heads, d, window,
+                                                       sinks), device)
+
+
+def window_attn_decode_workspace(b: int, cap: int, heads: int, kv_heads: int, d: int, window: int,
+                                 sinks: int = 0, device="cuda") -> torch.Tensor:
+    """Workspace of tp_window_attn_decode."""
+    return _bytes(load().tp_window_decode_workspace_size(b, cap, heads, kv_heads, d, window,
+                                                         sinks), device)
 
 
 def tp_device_status(stream=None) -> None:

@@ -944,6 +944,82 @@ tp_status qk_rope(const QkRope& r, bool bwd, void* ws, size_t ws_bytes, cudaStre
   return launch_qk_rope(r, bwd, ws, stream);
 }
 
+// -------------------------------------------------------- window attention
+
+// Sizes shared by the three calls; s: keys per sequence (sk, or cap).
+tp_status window_sizes(int64_t b, int64_t s, int heads, int kv_heads, int d, int64_t& window,
+                       int64_t& sinks) {
+  if (b <= 0 || s <= 0 || heads <= 0 || kv_heads <= 0)
+    return fail(TP_ERR_SHAPE, "batch, lengths and heads must be positive");
+  if (heads % kv_heads != 0) return fail(TP_ERR_SHAPE, "heads must be divisible by kv_heads");
+  if (d != 64 && d != 128) return fail(TP_ERR_UNSUPPORTED, "head dimension must be 64 or 128");
+  if (window < 1 || sinks < 0) return fail(TP_ERR_SHAPE, "window must be >= 1 and sinks >= 0");
+  if (!dims_ok({b, s, int64_t(heads) * d}) || b > kMaxDim / heads || b > kMaxDim / s)
+    return fail(TP_ERR_SHAPE, "sizes must be below 2^31 - 256");
+  if (window >= s) {  // full causal: the sinks are in the window
+    window = s;
+    sinks = 0;
+  }
+  if (sinks > s) sinks = s;
+  return TP_OK;
+}
+
+tp_status window_scale(float& scale, int d) {
+  if (!(scale >= 0.0f) || scale > 3.0e38f)
+    return fail(TP_ERR_SHAPE, "scale must be finite and not negative");
+  if (scale == 0.0f) scale = d == 64 ? 0.125f : 0.088388347648318447f;
+  return TP_OK;
+}
+
+tp_status window_attn_sizes(WindowAttn& w) {
+  if (w.sq <= 0) return fail(TP_ERR_SHAPE, "batch, lengths and heads must be positive");
+  TP_TRY(window_sizes(w.b, w.sk, w.heads, w.kv_heads, w.d, w.window, w.sinks));
+  if (!dims_ok({w.sq}) || w.b > kMaxDim / w.sq)
+    return fail(TP_ERR_SHAPE, "sizes must be below 2^31 - 256");
+  return window_attn_check(w);
+}
+
+tp_status window_attn(WindowAttn& w, bool bwd, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!w.q || !w.k || !w.v || !w.o || !w.lse) return fail(TP_ERR_NULL, "Q, K, V, O and LSE are required");
+  if (bwd && (!w.d_o || !w.dq || !w.dk || !w.dv))
+    return fail(TP_ERR_NULL, "dO, dQ, dK and dV are required");
+  TP_TRY(check_half_dtype(w.dtype));
+  TP_TRY(window_attn_sizes(w));
+  TP_TRY(window_scale(w.scale, w.d));
+  const int64_t nq = int64_t(w.heads) * w.d, nk = int64_t(w.kv_heads) * w.d;
+  for (int64_t ld : {w.ldq, w.ldo}) TP_TRY(check_ld(ld, nq));
+  for (int64_t ld : {w.ldk, w.ldv}) TP_TRY(check_ld(ld, nk));
+  if (bwd) {
+    for (int64_t ld : {w.lddo, w.lddq}) TP_TRY(check_ld(ld, nq));
+    for (int64_t ld : {w.lddk, w.lddv}) TP_TRY(check_ld(ld, nk));
+  }
+  TP_TRY(check_ptrs_aligned({w.q, w.k, w.v, w.o, w.lse, w.d_o, w.dq, w.dk, w.dv, ws}));
+  if (!bwd) return launch_window_attn_fwd(w, stream);
+  if (ws == nullptr || ws_bytes < window_attn_scratch_bytes(w))
+    return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_window_attn_workspace_size()");
+  return launch_window_attn_bwd(w, ws, stream);
+}
+
+tp_status window_decode(WindowDecode& w, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!w.q || !w.k || !w.v || !w.o || !w.lens)
+    return fail(TP_ERR_NULL, "Q, K, V, lens and O are required");
+  TP_TRY(check_half_dtype(w.dtype));
+  TP_TRY(window_sizes(w.b, w.cap, w.heads, w.kv_heads, w.d, w.window, w.sinks));
+  TP_TRY(window_scale(w.scale, w.d));
+  const int64_t nq = int64_t(w.heads) * w.d, nk = int64_t(w.kv_heads) * w.d;
+  for (int64_t ld : {w.ldq, w.ldo}) TP_TRY(check_ld(ld, nq));
+  for (int64_t ld : {w.ldk, w.ldv}) TP_TRY(check_ld(ld, nk));
+  for (int64_t bs : {w.bsk, w.bsv}) {
+    if (bs < 0 || bs > (int64_t(1) << 46)) return fail(TP_ERR_SHAPE, "batch stride out of range");
+    if (bs % 8 != 0) return fail(TP_ERR_ALIGN, "batch stride not a multiple of 8 elements");
+  }
+  TP_TRY(check_ptrs_aligned({w.q, w.k, w.v, w.o, w.lse, w.lens, ws}));
+  if (ws == nullptr || ws_bytes < window_decode_scratch_bytes(w))
+    return fail(TP_ERR_WORKSPACE,
+                "workspace missing or smaller than tp_window_decode_workspace_size()");
+  return launch_window_decode(w, ws, stream);
+}
+
 }  // namespace
 }  // namespace tp
 
@@ -1121,6 +1197,82 @@ tp_status tp_qk_norm_rope_bwd(const void* Q, int64_t ldq, const void* K, int64_t
            r.heads = heads; r.kv_heads = kv_heads; r.d = d; r.d_rot = d_rot; r.norm = norm;
            r.interleaved = interleaved; r.eps = eps; r.dtype = dtype;
            return qk_rope(r, true, ws, ws_bytes, static_cast<cudaStream_t>(stream));)
+}
+
+tp_status tp_window_attn_fwd(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, void* O, int64_t ldo, float* LSE, int64_t b, int64_t sq,
+                             int64_t sk, int heads, int kv_heads, int d, int64_t window,
+                             int64_t sinks, float scale, tp_dtype dtype, void* stream) {
+  TP_GUARD(WindowAttn w; w.q = Q; w.ldq = ldq; w.k = K; w.ldk = ldk; w.v = V; w.ldv = ldv; w.o = O;
+           w.ldo = ldo; w.lse = LSE; w.b = b; w.sq = sq; w.sk = sk; w.heads = heads;
+           w.kv_heads = kv_heads; w.d = d; w.window = window; w.sinks = sinks; w.scale = scale;
+           w.dtype = dtype;
+           return window_attn(w, false, nullptr, 0, static_cast<cudaStream_t>(stream));)
+}
+
+tp_status tp_window_attn_bwd(const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                             int64_t ldv, const void* O, int64_t ldo, const float* LSE,
+                             const void* dO, int64_t lddo, void* dQ, int64_t lddq, void* dK,
+                             int64_t lddk, void* dV, int64_t lddv, int64_t b, int64_t sq,
+                             int64_t sk, int heads, int kv_heads, int d, int64_t window,
+                             int64_t sinks, float scale, tp_dtype dtype, void* ws, size_t ws_bytes,
+                             void* stream) {
+  TP_GUARD(WindowAttn w; w.q = Q; w.ldq = ldq; w.k = K; w.ldk = ldk; w.v = V; w.ldv = ldv; w.o = O;
+           w.ldo = ldo; w.lse = LSE; w.d_o = dO; w.lddo = lddo; w.dq = dQ; w.lddq = lddq;
+           w.dk = dK; w.lddk = lddk; w.dv = dV; w.lddv = lddv; w.b = b; w.sq = sq; w.sk = sk;
+           w.heads = heads; w.kv_heads = kv_heads; w.d = d; w.window = window; w.sinks = sinks;
+           w.scale = scale; w.dtype = dtype;
+           return window_attn(w, true, ws, ws_bytes, static_cast<cudaStream_t>(stream));)
+}
+
+size_t tp_window_attn_workspace_size(int64_t b, int64_t sq, int64_t sk, int heads, int kv_heads,
+                                     int d, int64_t window, int64_t sinks) {
+  try {
+    WindowAttn w;
+    w.b = b;
+    w.sq = sq;
+    w.sk = sk;
+    w.heads = heads;
+    w.kv_heads = kv_heads;
+    w.d = d;
+    w.window = window;
+    w.sinks = sinks;
+    return window_attn_sizes(w) == TP_OK ? window_attn_scratch_bytes(w) : 0;
+  } catch (...) {
+    return 0;
+  }
+}
+
+tp_status tp_window_attn_decode(const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                                int64_t batch_k, const void* V, int64_t ldv, int64_t batch_v,
+                                const int32_t* lens, void* O, int64_t ldo, float* LSE, int64_t b,
+                                int64_t cap, int heads, int kv_heads, int d, int64_t window,
+                                int64_t sinks, float scale, tp_dtype dtype, void* ws,
+                                size_t ws_bytes, void* stream) {
+  TP_GUARD(WindowDecode w; w.q = Q; w.ldq = ldq; w.k = K; w.ldk = ldk; w.bsk = batch_k; w.v = V;
+           w.ldv = ldv; w.bsv = batch_v; w.lens = lens; w.o = O; w.ldo = ldo; w.lse = LSE; w.b = b;
+           w.cap = cap; w.heads = heads; w.kv_heads = kv_heads; w.d = d; w.window = window;
+           w.sinks = sinks; w.scale = scale; w.dtype = dtype;
+           return window_decode(w, ws, ws_bytes, static_cast<cudaStream_t>(stream));)
+}
+
+size_t tp_window_decode_workspace_size(int64_t b, int64_t cap, int heads, int kv_heads, int d,
+                                       int64_t window, int64_t sinks) {
+  try {
+    WindowDecode w;
+    w.b = b;
+    w.cap = cap;
+    w.heads = heads;
+    w.kv_heads = kv_heads;
+    w.d = d;
+    w.window = window;
+    w.sinks = sinks;
+    return window_sizes(b, cap, heads, kv_heads, d, w.window, w.sinks) == TP_OK
+               ? window_decode_scratch_bytes(w)
+               : 0;
+  } catch (...) {
+    return 0;
+  }
 }
 
 size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, int t,

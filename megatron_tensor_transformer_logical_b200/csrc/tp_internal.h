@@ -211,6 +211,39 @@ struct QkRope {
 size_t qk_rope_bwd_scratch_bytes(int64_t d);
 tp_status launch_qk_rope(const QkRope& r, bool bwd, void* scratch, cudaStream_t stream);
 
+// Attention over a sliding window with sinks (tp_window_attn_fwd / _bwd);
+// window and sinks are clamped to sk.
+struct WindowAttn {
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *o = nullptr, *d_o = nullptr;
+  const float* lse = nullptr;
+  void *dq = nullptr, *dk = nullptr, *dv = nullptr;
+  int64_t ldq = 0, ldk = 0, ldv = 0, ldo = 0, lddo = 0, lddq = 0, lddk = 0, lddv = 0;
+  int64_t b = 0, sq = 0, sk = 0, window = 0, sinks = 0;
+  int heads = 0, kv_heads = 0, d = 0;
+  float scale = 0.0f;
+  tp_dtype dtype = TP_BF16;
+};
+tp_status window_attn_check(const WindowAttn& w);  // launch limits
+size_t window_attn_scratch_bytes(const WindowAttn& w);
+tp_status launch_window_attn_fwd(const WindowAttn& w, cudaStream_t stream);
+tp_status launch_window_attn_bwd(const WindowAttn& w, void* scratch, cudaStream_t stream);
+
+// The same for one query per sequence over a cache (tp_window_attn_decode);
+// window and sinks are clamped to cap.
+struct WindowDecode {
+  const void *q = nullptr, *k = nullptr, *v = nullptr;
+  const int* lens = nullptr;
+  void* o = nullptr;
+  float* lse = nullptr;
+  int64_t ldq = 0, ldo = 0, ldk = 0, ldv = 0, bsk = 0, bsv = 0;
+  int64_t b = 0, cap = 0, window = 0, sinks = 0;
+  int heads = 0, kv_heads = 0, d = 0;
+  float scale = 0.0f;
+  tp_dtype dtype = TP_BF16;
+};
+size_t window_decode_scratch_bytes(const WindowDecode& w);
+tp_status launch_window_decode(const WindowDecode& w, void* scratch, cudaStream_t stream);
+
 // Attention core (per head causal softmax attention), bf16 with d = 128.
 struct AttnShape {
   int64_t b = 0, s = 0, h = 0;

@@ -1,0 +1,1448 @@
+// Attention over a sliding window with sinks on the sm_100a tensor cores:
+// forward and backward (tp_window_attn_fwd / _bwd).
+//
+//   O = softmax(scale Q K^T) V per head, where query r of a sequence sits at
+//   position p = r + sk - sq and sees key c when
+//     c <= p  and  (p - c < window  or  c < sinks).
+//   Query head j reads key / value head j / G, G = heads / kv_heads.
+// Backward, with P the probabilities and D = rowsum(dO * O):
+//   dS = P (dO V^T - D),  dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
+//   dK and dV summed over the G query heads that share them.
+//
+// Same tile machinery as the full causal core (tp_attention_sm100.cu): TMA
+// into 128-byte-swizzled shared memory, tcgen05 products with S, P and the
+// accumulators in tensor memory, one row per thread in the softmax.  What the
+// window changes:
+// * Work per query tile is the key blocks of [first visible, diagonal] plus
+//   the sink blocks in front of them; blocks in between are never loaded.
+//   The two query tiles of a CTA share one list of blocks and each takes part
+//   in those it sees.
+// * A 32-column chunk a row sees whole takes the unmasked path; the others
+//   (window edge, diagonal, sinks) go through a 32-bit visibility mask.
+// * A row may see nothing in a block (its window starts later) or at all
+//   (p < 0): the running maximum then stays -inf and P is 0, and a row that
+//   saw nothing ends with O = 0 and LSE = -inf.
+// * dK / dV: a key tile's queries are one contiguous range, [k0, k1 + window),
+//   or everything after it where the tile holds sinks.  The heads of a group
+//   follow one another in one accumulation (fixed order, no atomics).  Tiles
+//   whose queries take long (sinks, wide windows, few heads) are cut along
+//   (head, query) into slices with fp32 partials that a last kernel adds in
+//   slice order, so no SM is left with one long tile at the end.
+// * Sequences are the third dimension of the tensor maps: rows past a
+//   sequence's end read as zero, never as its neighbour's values.
+//
+// bf16 and fp16 inputs; P and dS are rounded to the input type for their
+// products (fp32 accumulation), as the products take one type for both
+// operands.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "attn_sm100.cuh"
+#include "ptx_sm100.cuh"
+#include "tp_internal.h"
+
+namespace tp {
+namespace {
+
+constexpr int kBM = 128;  // query rows per tile
+constexpr int kBN = 128;  // keys per block (forward), keys per tile (dK / dV)
+constexpr int kB64 = 64;  // keys per block (dQ), queries per block (dK / dV)
+constexpr int kThreads = 384;
+constexpr float kRescaleLog2 = 8.0f;  // O keeps a stale maximum up to 2^8 behind
+constexpr float kCheckSum = 255.0f;   // a row sum above this may hide such a key
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// kind::f16 descriptor: fp16 operands, or bf16 ones.
+template <bool BF>
+__host__ __device__ constexpr uint32_t idesc(int m, int n, bool a_mn, bool b_mn) {
+  return BF ? idesc_bf16_f32(m, n, a_mn, b_mn) : idesc_f16_f32(m, n, a_mn, b_mn);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if (BF) {
+    __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&t);
+  }
+  return pack_half2(a, b);
+}
+
+template <bool BF>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if (BF) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Eight fp32 values as one 16-byte store of the input type.
+template <bool BF>
+__device__ __forceinline__ uint4 pack8t(const float* v, float f) {
+  return make_uint4(pack2<BF>(v[0] * f, v[1] * f), pack2<BF>(v[2] * f, v[3] * f),
+                    pack2<BF>(v[4] * f, v[5] * f), pack2<BF>(v[6] * f, v[7] * f));
+}
+
+struct WinArgs {
+  int sq, sk, off;  // off = sk - sq: query r sits at position r + off
+  int heads, kv_heads, group;
+  int window, sinks;  // both clamped to sk
+  float scale, scale_log2;
+  void* o;
+  long long ldo;
+  float* lse;  // [b, heads, sq]
+  // backward
+  const float* nlse;  // -LSE * log2(e) and -D: [b * heads] rows of sp floats,
+  const float* nd;    // zero beyond sq, 64 zeros after the last row
+  int sp;
+  void *dq, *dk, *dv;
+  long long lddq, lddk, lddv;
+  // dK / dV items: nsink_tiles key tiles hold sinks; the two classes of tiles
+  // are cut into split_s and split_w slices; partials of cut tiles in part.
+  int bkv, key_tiles, sink_tiles, split_s, split_w, items;
+  float* part;
+  WaitCtl status;
+};
+
+// Key blocks of BN that some row of the query tile [r0, r0 + 128) sees
+// through the window: [lo, hi], hi = -1 when the tile sees no key.  Every
+// block in front of them that holds a sink is seen too.
+struct Blocks {
+  int lo, hi;
+};
+
+template <int BN>
+__device__ __forceinline__ Blocks blocks_of(int r0, const WinArgs& a) {
+  const int r1 = min(r0 + kBM, a.sq) - 1;
+  Blocks b;
+  const int p1 = r1 + a.off;
+  if (r1 < r0 || p1 < 0) {
+    b.lo = 0;
+    b.hi = -1;
+  } else {
+    b.lo = max(0, r0 + a.off - a.window + 1) / BN;
+    b.hi = p1 / BN;
+  }
+  return b;
+}
+
+// The CTA's list of key blocks for its two query tiles: sink blocks [0, ns),
+// then [lo, hi].  Every listed block is seen by one of the tiles at least.
+template <int BN>
+struct BlockList {
+  Blocks t0, t1;
+  int nsb, ns, lo, n;
+  __device__ __forceinline__ BlockList(int r0, const WinArgs& a) {
+    t0 = blocks_of<BN>(r0, a);
+    t1 = blocks_of<BN>(r0 + kBM, a);
+    nsb = (a.sinks + BN - 1) / BN;
+    lo = t0.lo;
+    const int hi = max(t0.hi, t1.hi);
+    ns = hi < 0 ? 0 : min(nsb, lo);
+    n = hi < 0 ? 0 : ns + hi - lo + 1;
+  }
+  __device__ __forceinline__ int block(int j) const { return j < ns ? j : lo + (j - ns); }
+  __device__ __forceinline__ bool sees(int x, int j) const {
+    const int kb = block(j);
+    const int xlo = x ? t1.lo : t0.lo, xhi = x ? t1.hi : t0.hi;
+    return kb <= xhi && (kb >= xlo || kb < nsb);
+  }
+  // listed blocks that tile x sees
+  __device__ __forceinline__ int count(int x) const {
+    const int xlo = x ? t1.lo : t0.lo, xhi = x ? t1.hi : t0.hi;
+    return xhi < 0 ? 0 : xhi + 1 - max(0, xlo - nsb);
+  }
+};
+
+// Visible columns of a row within one key block: [0, end) intersected with
+// [first, inf) or [0, sink).
+struct RowMask {
+  int end, first, sink;
+  // all of [c, c + 32) visible
+  __device__ __forceinline__ bool full(int c) const {
+    return c + 32 <= end && (c >= first || c + 32 <= sink);
+  }
+  // bit i: column c + i visible
+  __device__ __forceinline__ uint32_t bits(int c) const {
+    const uint32_t before_end = prefix(end - c);
+    return before_end & (~prefix(first - c) | prefix(sink - c));
+  }
+  static __device__ __forceinline__ uint32_t prefix(int n) {
+    return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+  }
+};
+
+// Row with query position p (p < sk) in the key block that starts at k0.
+__device__ __forceinline__ RowMask row_mask(int p, int k0, const WinArgs& a) {
+  RowMask m;
+  m.end = p + 1 - k0;
+  m.first = p - a.window + 1 - k0;
+  m.sink = a.sinks - k0;
+  return m;
+}
+
+// The maximum raw score among a row's visible keys of one block, -inf if none.
+__device__ __forceinline__ float row_max_masked(uint32_t srow, const RowMask& m) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < kBN; c += 32) {
+    float v[32];
+    tmem_ld32(srow + c, v);
+    if (!m.full(c)) {
+      const uint32_t vis = m.bits(c);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = ((vis >> i) & 1u) ? v[i] : -INFINITY;
+    }
+    mx = max32(v, mx);
+  }
+  return mx;
+}
+
+// P = 2^(s * scale_log2 - m) over one block row (hidden keys 0), packed in
+// registers; returns the row sum of the unrounded P.
+template <bool BF>
+__device__ __forceinline__ float exp_row_masked(uint32_t srow, const RowMask& mask,
+                                                float scale_log2, float m,
+                                                uint32_t (&pk)[kBN / 2]) {
+  const float2 sc2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m, -m);
+  float2 acc = make_float2(0.0f, 0.0f);
+  uint32_t nx[32];
+  tmem_ld32_nowait(srow, nx);
+  tmem_wait_ld(nx);
+#pragma unroll
+  for (int c = 0; c < kBN; c += 32) {
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(nx[i]);
+    if (c + 32 < kBN) tmem_ld32_nowait(srow + c + 32, nx);
+    float2 u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float2 t = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
+      u[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+    }
+    if (!mask.full(c)) {
+      const uint32_t vis = mask.bits(c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        u[i] = make_float2((vis >> (2 * i)) & 1u ? u[i].x : 0.0f,
+                           (vis >> (2 * i + 1)) & 1u ? u[i].y : 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pk[c / 2 + i] = pack2<BF>(u[i].x, u[i].y);
+#pragma unroll
+    for (int k = 8; k >= 1; k >>= 1)
+#pragma unroll
+      for (int i = 0; i < k; ++i) u[i] = __fadd2_rn(u[i], u[i + k]);
+    acc = __fadd2_rn(acc, u[0]);
+    if (c + 32 < kBN) tmem_wait_ld(nx);
+  }
+  return acc.x + acc.y;
+}
+
+// One box per 64 columns of a [rows x DH] tile; the halves are rows * 128
+// bytes apart.
+template <int DH>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, uint64_t* bar,
+                                          int head, int row, int seq, int rows) {
+#pragma unroll
+  for (int c = 0; c < DH / 64; ++c)
+    tma_load_3d(dst + c * rows * 128, map, bar, head * DH + 64 * c, row, seq);
+}
+
+// Byte offset of K step kk (16 columns) in a K-major tile of `rows` rows.
+__device__ __forceinline__ uint32_t k_off(int kk, int rows) {
+  return static_cast<uint32_t>((kk >> 2) * rows * 128 + (kk & 3) * 32);
+}
+
+template <int DH>
+struct FwdSmem {
+  static constexpr int kTile = 128 * DH * 2;
+  static constexpr int kBytes = 1024 + 6 * kTile + 256;  // Q[2], K[2], V[2], barriers
+};
+
+// One CTA per (sequence, head, pair of adjacent 128-row query tiles), as in
+// the full causal core: warp 0 TMA, warp 1 tensor memory and MMA issue, warps
+// 4-7 / 8-11 the softmax of tile 0 / 1.
+template <bool BF, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const WinArgs a) {
+  constexpr int kTile = FwdSmem<DH>::kTile;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;              // [2] query tiles
+  uint8_t* sK = smem + 2 * kTile;  // [2] stages
+  uint8_t* sV = smem + 4 * kTile;  // [2] stages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 6 * kTile);
+  uint64_t* q_full = bars + 0;
+  uint64_t* k_full = bars + 1;   // [2] stages
+  uint64_t* k_empty = bars + 3;  // [2]
+  uint64_t* v_full = bars + 5;   // [2]
+  uint64_t* v_empty = bars + 7;  // [2]
+  uint64_t* s_full = bars + 9;   // [2] tiles: S ready (and the previous P V done)
+  uint64_t* p_full = bars + 11;  // [2] tiles: P stored (and O rescaled)
+  uint64_t* o_full = bars + 13;  // [2] tiles: P V done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int npairs = ((a.sq + kBM - 1) / kBM + 1) / 2;
+  const int pair = npairs - 1 - static_cast<int>(blockIdx.y);  // longest rows first
+  const int head = blockIdx.x % a.heads, bi = blockIdx.x / a.heads;
+  const int kvh = head / a.group;
+  const int r0 = 2 * pair * kBM;
+  const BlockList<kBN> bl(r0, a);
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);  // one arrival per warp of the tile's softmax group
+      mbar_init(&o_full[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Tile x: S_x at columns [256 x, +128) (P_x over its first 64), O_x at
+  // [256 x + 128, + DH).
+  auto tS = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x); };
+  auto tO = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
+
+  if (warp == 0) {
+    if (lane == 0 && bl.n > 0) {
+      // ------------------------------------------------------- TMA producer
+      bool ok = true;
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const int tiles = r0 + kBM < a.sq ? 2 : 1;
+      mbar_arrive_expect_tx(q_full, tiles * kTile);
+      for (int x = 0; x < tiles; ++x)
+        load_tile<DH>(sQ + x * kTile, &tmQ, q_full, head, r0 + x * kBM, bi, 128);
+      for (int j = 0; j < bl.n && ok; ++j) {
+        const int st = j & 1;
+        const uint32_t ph = static_cast<uint32_t>(j >> 1) & 1u;
+        const int krow = bl.block(j) * kBN;
+        if (!(ok = mbar_wait(&k_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
+        mbar_arrive_expect_tx(&k_full[st], kTile);
+        load_tile<DH>(sK + st * kTile, &tmK, &k_full[st], kvh, krow, bi, 128);
+        if (!(ok = mbar_wait(&v_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
+        mbar_arrive_expect_tx(&v_full[st], kTile);
+        load_tile<DH>(sV + st * kTile, &tmV, &v_full[st], kvh, krow, bi, 128);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && bl.n > 0) {
+      // --------------------------------------------------------- MMA issuer
+      // Per listed block j and tile that sees it: P_x V_j; then S_x of block
+      // j + 1 if the tile sees that.  The MMAs run in issue order, so S_x
+      // overwrites P_x only after its product has read it, and the commit of
+      // S_x also covers the tile's previous P V.
+      constexpr uint32_t kIdS = idesc<BF>(128, 128, false, false);  // Q K^T
+      constexpr uint32_t kIdO = idesc<BF>(128, DH, false, true);    // P V
+      auto issue_s = [&](int x, int j) {
+        const uint32_t q_addr = smem_u32(sQ + x * kTile);
+        const uint32_t k_addr = smem_u32(sK + (j & 1) * kTile);
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk)
+          umma_bf16(tS(x), sw128_desc(q_addr + k_off(kk, 128), 16, 1024),
+                    sw128_desc(k_addr + k_off(kk, 128), 16, 1024), kIdS, kk > 0 ? 1u : 0u);
+        umma_commit(&s_full[x]);
+      };
+      int done[2] = {0, 0};  // P V products issued per tile
+      bool ok = mbar_wait(q_full, 0, a.status, kStatusAttnTimeout);
+      for (int j = -1; j < bl.n && ok; ++j) {
+        const int st = j & 1;
+        if (j >= 0 && !(ok = mbar_wait(&v_full[st], static_cast<uint32_t>(j >> 1) & 1u, a.status,
+                                       kStatusAttnTimeout)))
+          break;
+        const bool more = j + 1 < bl.n;
+        bool k_next = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) break;
+          if (j >= 0 && bl.sees(x, j)) {
+            if (!(ok = mbar_wait(&p_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
+                                 kStatusAttnTimeout)))
+              break;
+            tc_fence_after();
+            const uint32_t v_addr = smem_u32(sV + st * kTile);
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)  // 16 keys: 8 columns of pairs
+              umma_f16_ts(tO(x), tS(x) + static_cast<uint32_t>(kk * 8),
+                          sw128_desc(v_addr + kk * 16 * 128, 128 * 128, 1024), kIdO,
+                          (done[x] > 0 || kk > 0) ? 1u : 0u);
+            umma_commit(&o_full[x]);
+            ++done[x];
+          }
+          if (more && bl.sees(x, j + 1)) {
+            if (!k_next) {
+              if (!(ok = mbar_wait(&k_full[(j + 1) & 1], static_cast<uint32_t>((j + 1) >> 1) & 1u,
+                                   a.status, kStatusAttnTimeout)))
+                break;
+              tc_fence_after();
+              k_next = true;
+            }
+            issue_s(x, j + 1);
+          }
+        }
+        if (!ok) break;
+        if (more) umma_commit(&k_empty[(j + 1) & 1]);
+        if (j >= 0) umma_commit(&v_empty[st]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ----------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = r0 + x * kBM + quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t srow = tS(x) + lane_off, orow_t = tO(x) + lane_off;
+    // Rows past the end take the last position: their results are not stored.
+    const int p = min(r, a.sq - 1) + a.off;
+    const int total = bl.count(x);
+    float m_used = -INFINITY, l_run = 0.0f;
+    bool ok = true;
+    int cnt = 0;
+    for (int j = 0; j < bl.n && cnt < total; ++j) {
+      if (!bl.sees(x, j)) continue;
+      if (!(ok = mbar_wait(&s_full[x], static_cast<uint32_t>(cnt) & 1u, a.status,
+                           kStatusAttnTimeout)))
+        break;
+      tc_fence_after();
+      const RowMask mask = row_mask(p, bl.block(j) * kBN, a);
+      if (cnt == 0) m_used = row_max_masked(srow, mask) * a.scale_log2;
+      uint32_t pk[kBN / 2];
+      // A row that has seen no key yet (m_used = -inf) has P = 0 by the mask;
+      // 0 stands in for its maximum.
+      float rs = exp_row_masked<BF>(srow, mask, a.scale_log2,
+                                    m_used == -INFINITY ? 0.0f : m_used, pk);
+      // The first block set the maximum in use, so its P <= 1.  Later blocks:
+      // a row sum above kCheckSum, or a row without a maximum so far, sends
+      // the warp to the exact maximum.
+      if (cnt > 0 && __any_sync(0xffffffffu, rs > kCheckSum || m_used == -INFINITY)) {
+        const float m_new = row_max_masked(srow, mask) * a.scale_log2;
+        const bool need = m_new > m_used + kRescaleLog2;
+        if (__any_sync(0xffffffffu, need)) {
+          // Recompute P at the new maximum (S is intact: P has not been
+          // stored) and rescale O (the tile's previous P V completed before
+          // this S) and l.  From -inf the factor is 0, on sums that are 0.
+          const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
+          if (need) m_used = m_new;
+          rs = exp_row_masked<BF>(srow, mask, a.scale_log2, m_used == -INFINITY ? 0.0f : m_used,
+                                  pk);
+#pragma unroll 1
+          for (int c = 0; c < DH; c += 32) {
+            float o[32];
+            tmem_ld32(orow_t + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st32(orow_t + c, o);
+          }
+          l_run *= alpha;
+        }
+      }
+      l_run += rs;
+#pragma unroll
+      for (int c = 0; c < kBN / 2; c += 16) {
+        uint32_t q16[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q16[i] = pk[c + i];
+        tmem_st16(srow + c, q16);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[x]);
+      ++cnt;
+    }
+    if (ok && total > 0)
+      ok = mbar_wait(&o_full[x], static_cast<uint32_t>(total - 1) & 1u, a.status,
+                     kStatusAttnTimeout);
+    if (ok) {
+      if (total > 0) tc_fence_after();
+      const bool some = l_run > 0.0f;
+      const float inv = some ? 1.0f / l_run : 0.0f;
+      uint8_t* orow = static_cast<uint8_t*>(a.o) +
+                      ((static_cast<long long>(bi) * a.sq + r) * a.ldo + head * DH) * 2;
+#pragma unroll 1
+      for (int c = 0; c < DH; c += 32) {
+        float v[32];
+        if (total > 0) tmem_ld32(orow_t + c, v);
+        if (!some) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+        if (r < a.sq) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(orow + 2 * (c + 8 * q)) = pack8t<BF>(v + 8 * q, inv);
+        }
+      }
+      if (r < a.sq)
+        a.lse[(static_cast<long long>(bi) * a.heads + head) * a.sq + r] =
+            some ? (m_used + log2f(l_run)) * kLn2 : -INFINITY;
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ backward
+
+// Row terms of the backward: nd = -rowsum(dO * O), nlse = -LSE * log2(e); a
+// row that saw no key (LSE = -inf) gets nlse = -inf, i.e. P = 0.  DH / 8
+// threads per (row, head) with 16-byte loads; the same threads zero the row
+// padding and the 64-float tail.  HBM-bound: 4 bytes read per element.
+template <bool BF, int DH>
+__global__ void __launch_bounds__(256)
+    window_dsum(const void* o, long long ldo, const void* d_o, long long lddo, const float* lse,
+                float* nlse, float* nd, long long rows, int sq, int heads, int sp) {
+  constexpr int kLanes = DH / 8;
+  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const long long pair = t / kLanes;  // (row, head), head fastest
+  const int l = threadIdx.x & (kLanes - 1);
+  const bool in = pair < rows * heads;
+  float acc = 0.0f, ls = 0.0f;
+  long long dst = 0;
+  if (in) {
+    const long long row = pair / heads;
+    const int head = static_cast<int>(pair - row * heads);
+    const long long bi = row / sq, r = row - bi * sq;
+    const long long q = bi * heads + head;
+    dst = q * sp + r;
+    if (l == 0) ls = lse[q * sq + r];
+    const uint4 ov = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o) + row * ldo +
+                                                     head * DH + l * 8);
+    const uint4 dv = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d_o) +
+                                                     row * lddo + head * DH + l * 8);
+    const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<BF>(ow[i]), y = unpack2<BF>(dw[i]);
+      acc = fmaf(x.x, y.x, acc);
+      acc = fmaf(x.y, y.y, acc);
+    }
+  }
+#pragma unroll
+  for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+  if (in && l == 0) {
+    nd[dst] = -acc;
+    nlse[dst] = ls == -INFINITY ? -INFINITY : -(ls * kLog2e);
+  }
+  const long long bh = rows / sq * heads;
+  const int padr = sp - sq;
+  if (t < bh * padr) {
+    const long long i = t / padr * sp + sq + t % padr;
+    nd[i] = 0.0f;
+    nlse[i] = 0.0f;
+  } else if (t < bh * padr + 64) {
+    const long long i = bh * sp + (t - bh * padr);
+    nd[i] = 0.0f;
+    nlse[i] = 0.0f;
+  }
+}
+
+constexpr int kKvStages = 3;
+
+template <int DH>
+struct DqSmem {
+  static constexpr int kTile = 128 * DH * 2, kTile64 = 64 * DH * 2;
+  // Q[2] | dO[2] | ring of (K, V) | barriers
+  static constexpr int kBytes = 1024 + 4 * kTile + kKvStages * 2 * kTile64 + 256;
+};
+
+// dQ: one CTA per (sequence, head, pair of query tiles), 64-key blocks.  Per
+// block and tile: S = Q K^T, dP = dO V^T -> dS over S -> dQ += dS K.
+template <bool BF, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const WinArgs a) {
+  constexpr int kTile = DqSmem<DH>::kTile, kTile64 = DqSmem<DH>::kTile64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = smem;               // [2] tiles
+  uint8_t* sdO = smem + 2 * kTile;  // [2] tiles
+  uint8_t* sKV = smem + 4 * kTile;  // stage st: K at +0, V at +kTile64
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kKvStages * (2 * kTile64));
+  uint64_t* qd_full = bars + 0;
+  uint64_t* kv_full = bars + 1;              // [kKvStages]
+  uint64_t* kv_empty = kv_full + kKvStages;  // [kKvStages]
+  uint64_t* s_full = kv_empty + kKvStages;   // [2] tiles: S, dP ready
+  uint64_t* ds_full = s_full + 2;            // [2] tiles: dS stored
+  uint64_t* dq_done = ds_full + 2;           // [2] tiles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dq_done + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int npairs = ((a.sq + kBM - 1) / kBM + 1) / 2;
+  const int pair = npairs - 1 - static_cast<int>(blockIdx.y);
+  const int head = blockIdx.x % a.heads, bi = blockIdx.x / a.heads;
+  const int kvh = head / a.group;
+  const int r0 = 2 * pair * kBM;
+  const BlockList<kB64> bl(r0, a);
+
+  if (threadIdx.x == 0) {
+    mbar_init(qd_full, 1);
+    for (int i = 0; i < kKvStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&ds_full[i], 4);  // the tile's four element-wise warps
+      mbar_init(&dq_done[i], 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // Tile x: S_x at [256 x, +64) (dS_x over its first 32 columns), dP_x at
+  // [256 x + 64, +64), dQ_x at [256 x + 128, + DH).
+  auto tS = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x); };
+  auto tP = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 64); };
+  auto tQ = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
+
+  if (warp == 0) {
+    if (lane == 0 && bl.n > 0) {
+      bool ok = true;
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmdO);
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      const int tiles = r0 + kBM < a.sq ? 2 : 1;
+      mbar_arrive_expect_tx(qd_full, tiles * 2 * kTile);
+      for (int x = 0; x < tiles; ++x) {
+        load_tile<DH>(sQ + x * kTile, &tmQ, qd_full, head, r0 + x * kBM, bi, 128);
+        load_tile<DH>(sdO + x * kTile, &tmdO, qd_full, head, r0 + x * kBM, bi, 128);
+      }
+      for (int j = 0; j < bl.n && ok; ++j) {
+        const int ks = j % kKvStages;
+        const uint32_t kph = static_cast<uint32_t>(j / kKvStages) & 1u;
+        if (!(ok = mbar_wait(&kv_empty[ks], kph ^ 1u, a.status, kStatusAttnTimeout))) break;
+        mbar_arrive_expect_tx(&kv_full[ks], 2 * kTile64);
+        uint8_t* dst = sKV + ks * (2 * kTile64);
+        const int krow = bl.block(j) * kB64;
+        load_tile<DH>(dst, &tmK, &kv_full[ks], kvh, krow, bi, 64);
+        load_tile<DH>(dst + kTile64, &tmV, &kv_full[ks], kvh, krow, bi, 64);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && bl.n > 0) {
+      constexpr uint32_t kIdSP = idesc<BF>(128, 64, false, false);  // Q K^T, dO V^T
+      constexpr uint32_t kIdQ = idesc<BF>(128, DH, false, true);    // dS K
+      auto issue_sp = [&](int x, int j) {
+        const uint32_t q_addr = smem_u32(sQ + x * kTile), do_addr = smem_u32(sdO + x * kTile);
+        const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
+        const uint32_t v_addr = k_addr + kTile64;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          umma_bf16(tS(x), sw128_desc(q_addr + k_off(kk, 128), 16, 1024),
+                    sw128_desc(k_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+          umma_bf16(tP(x), sw128_desc(do_addr + k_off(kk, 128), 16, 1024),
+                    sw128_desc(v_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[x]);
+      };
+      const int total[2] = {bl.count(0), bl.count(1)};
+      int done[2] = {0, 0};
+      bool ok = mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
+      for (int j = -1; j < bl.n && ok; ++j) {
+        const bool more = j + 1 < bl.n;
+        bool kv_next = false;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (!ok) break;
+          if (j >= 0 && bl.sees(x, j)) {
+            if (!(ok = mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
+                                 kStatusAttnTimeout)))
+              break;
+            tc_fence_after();
+            const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
+#pragma unroll
+            for (int kk = 0; kk < kB64 / 16; ++kk)
+              umma_f16_ts(tQ(x), tS(x) + static_cast<uint32_t>(kk * 8),
+                          sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ,
+                          (done[x] > 0 || kk > 0) ? 1u : 0u);
+            if (++done[x] == total[x]) umma_commit(&dq_done[x]);
+          }
+          if (more && bl.sees(x, j + 1)) {
+            if (!kv_next) {
+              const int ks = (j + 1) % kKvStages;
+              if (!(ok = mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
+                                   a.status, kStatusAttnTimeout)))
+                break;
+              tc_fence_after();
+              kv_next = true;
+            }
+            issue_sp(x, j + 1);
+          }
+        }
+        if (!ok) break;
+        if (j >= 0) umma_commit(&kv_empty[j % kKvStages]);
+      }
+    }
+  } else if (warp >= 4) {
+    const int x = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = r0 + x * kBM + quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const long long stat = (static_cast<long long>(bi) * a.heads + head) * a.sp;
+    const int rc = min(r, a.sq - 1);
+    const float nl = a.nlse[stat + rc], ndd = a.nd[stat + rc];
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+    const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(ndd, ndd);
+    const int p = rc + a.off;
+    const int total = bl.count(x);
+    bool ok = true;
+    int cnt = 0;
+    for (int j = 0; j < bl.n && cnt < total; ++j) {
+      if (!bl.sees(x, j)) continue;
+      if (!(ok = mbar_wait(&s_full[x], static_cast<uint32_t>(cnt) & 1u, a.status,
+                           kStatusAttnTimeout)))
+        break;
+      tc_fence_after();
+      const RowMask mask = row_mask(p, bl.block(j) * kB64, a);
+#pragma unroll
+      for (int c = 0; c < kB64; c += 32) {
+        float sv[32], pv[32];
+        tmem_ld32x2(tS(x) + lane_off + c, sv, tP(x) + lane_off + c, pv);
+        uint32_t pk[16];
+        const uint32_t vis = mask.full(c) ? 0xffffffffu : mask.bits(c);
+        if (vis == 0xffffffffu) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
+            const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+            const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+            pk[i >> 1] = pack2<BF>(g.x, g.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
+            const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
+                                         (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
+            const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+            pk[i >> 1] = pack2<BF>(g.x, g.y);
+          }
+        }
+        // dS columns [c / 2, c / 2 + 16): S columns this thread has read.
+        tmem_st16(tS(x) + lane_off + c / 2, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ds_full[x]);
+      ++cnt;
+    }
+    if (ok && total > 0) ok = mbar_wait(&dq_done[x], 0, a.status, kStatusAttnTimeout);
+    if (ok) {
+      if (total > 0) tc_fence_after();
+      uint8_t* out = static_cast<uint8_t*>(a.dq) +
+                     ((static_cast<long long>(bi) * a.sq + r) * a.lddq + head * DH) * 2;
+#pragma unroll 1
+      for (int cc = 0; cc < DH; cc += 32) {
+        float v[32];
+        if (total > 0) {
+          tmem_ld32(tQ(x) + lane_off + cc, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+        }
+        if (r < a.sq) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(out + 2 * (cc + 8 * q)) = pack8t<BF>(v + 8 * q, a.scale);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+constexpr int kQdStages = 4;
+
+template <int DH>
+struct KvSmem {
+  static constexpr int kTile = 128 * DH * 2, kTile64 = 64 * DH * 2;
+  // K | V | ring of (Q, dO) | barriers | ring of row terms (128 floats)
+  static constexpr int kBytes =
+      1024 + 2 * kTile + kQdStages * 2 * kTile64 + 256 + kQdStages * 2 * kB64 * 4;
+};
+
+// Query blocks of 64 that see some key of the tile at k0: [i0, i0 + n).
+struct QRange {
+  int i0, n;
+};
+
+__host__ __device__ __forceinline__ QRange query_blocks(int k0, int sq, int sk, int window,
+                                                        int sinks) {
+  const int off = sk - sq;
+  const int k1 = (k0 + kBN < sk ? k0 + kBN : sk) - 1;
+  const int lo = k0 - off > 0 ? k0 - off : 0;
+  int hi = sq - 1;
+  if (k0 >= sinks) {
+    const long long w = static_cast<long long>(k1) + window - 1 - off;
+    if (w < hi) hi = static_cast<int>(w);
+  }
+  QRange q;
+  q.i0 = lo / kB64;
+  q.n = lo <= hi ? hi / kB64 - q.i0 + 1 : 0;
+  return q;
+}
+
+// Work item k of the dK / dV kernel: a slice [j0, j1) of the (head, query
+// block) list of one (sequence, key head, key tile); list entry j is query
+// block i0 + j % n of head kvh * group + j / n.  The sink tiles' slices come
+// first (they are the longest).
+struct KvItem {
+  int bi, kvh, k0, i0, n, j0, j1;
+  int slot;  // slice of the partials, -1: the tile is not cut
+};
+
+__device__ __forceinline__ KvItem kv_item(int k, const WinArgs& a) {
+  KvItem it;
+  const int sink_items = a.sink_tiles * a.split_s * a.bkv;
+  int split, s, kb, bk;
+  if (k < sink_items) {
+    split = a.split_s;
+    bk = k % a.bkv;
+    const int v = k / a.bkv;
+    s = v % split;
+    kb = v / split;
+    it.slot = split > 1 ? (kb * a.bkv + bk) * split + s : -1;
+  } else {
+    const int v0 = k - sink_items;
+    split = a.split_w;
+    bk = v0 % a.bkv;
+    const int v = v0 / a.bkv;
+    s = v % split;
+    kb = v / split;  // among the tiles without sinks
+    it.slot = split > 1 ? (a.split_s > 1 ? sink_items : 0) + (kb * a.bkv + bk) * split + s : -1;
+    kb += a.sink_tiles;
+  }
+  it.kvh = bk % a.kv_heads;
+  it.bi = bk / a.kv_heads;
+  it.k0 = kb * kBN;
+  const QRange q = query_blocks(it.k0, a.sq, a.sk, a.window, a.sinks);
+  it.i0 = q.i0;
+  it.n = q.n;
+  const long long len = static_cast<long long>(q.n) * a.group;
+  it.j0 = static_cast<int>(s * len / split);
+  it.j1 = static_cast<int>((s + 1) * len / split);
+  return it;
+}
+
+// The r-th item of this CTA, or -1: rounds of gridDim.x items in snake order.
+__device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
+  const long long g = gridDim.x, c = blockIdx.x;
+  const long long k = r * g + ((r & 1) ? g - 1 - c : c);
+  return k < a.items ? static_cast<int>(k) : -1;
+}
+
+// Persistent dK / dV: one CTA per SM walks its items; per 64-query block
+// S^T = K Q^T, dP^T = V dO^T -> P^T, dS^T -> dV += P^T dO, dK += dS^T Q.
+// The Q / dO ring runs on across items; an item's K and V load once the
+// previous item's last S^T / dP^T are done (kv_empty), and its first dV, dK
+// products wait until the previous epilogue has read the accumulators
+// (acc_empty).  Items without queries only write zeros.
+template <bool BF, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd_dkdv(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                    const WinArgs a) {
+  constexpr int kTile = KvSmem<DH>::kTile, kTile64 = KvSmem<DH>::kTile64;
+  constexpr int kEwWarps = 8;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = smem + kTile;
+  uint8_t* sQdO = smem + 2 * kTile;  // stage q: Q at +0, dO at +kTile64
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sQdO + kQdStages * (2 * kTile64));
+  uint64_t* kv_full = bars + 0;
+  uint64_t* kv_empty = bars + 1;             // the item's last S^T / dP^T done
+  uint64_t* qd_full = bars + 2;              // [kQdStages]
+  uint64_t* qd_empty = qd_full + kQdStages;  // [kQdStages]
+  uint64_t* s_full = qd_empty + kQdStages;   // [2]
+  uint64_t* p_full = s_full + 2;             // [2]
+  uint64_t* acc_done = p_full + 2;           // the item's last dV, dK products done
+  uint64_t* acc_empty = acc_done + 1;        // the epilogue has read dV, dK
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
+  // stage q: -LSE * log2(e) of the block's 64 queries at [0, 64), -D at [64, 128)
+  float* s_stat = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    mbar_init(kv_empty, 1);
+    for (int i = 0; i < kQdStages; ++i) {
+      mbar_init(&qd_full[i], 1);
+      mbar_init(&qd_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], kEwWarps);
+    }
+    mbar_init(acc_done, 1);
+    mbar_init(acc_empty, kEwWarps);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // S^T buffers at columns 0 and 64, dP^T at 128 and 192, dV at 256, dK at 384.
+  auto tS = [tmem](int st) { return tmem + static_cast<uint32_t>(64 * st); };
+  auto tP = [tmem](int st) { return tmem + static_cast<uint32_t>(128 + 64 * st); };
+  const uint32_t tdV = tmem + 256, tdK = tmem + 384;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+      tma_prefetch_desc(&tmQ);
+      tma_prefetch_desc(&tmdO);
+      bool ok = true;
+      long long g = 0;  // query blocks loaded so far: the ring position
+      uint32_t it_no = 0;  // items with queries so far
+      for (int r = 0; ok; ++r) {
+        const int k = kv_item_index(r, a);
+        if (k < 0) break;
+        const KvItem it = kv_item(k, a);
+        if (it.j0 >= it.j1) continue;
+        if (!(ok = mbar_wait(kv_empty, (it_no & 1u) ^ 1u, a.status, kStatusAttnTimeout))) break;
+        ++it_no;
+        mbar_arrive_expect_tx(kv_full, 2 * kTile);
+        load_tile<DH>(sK, &tmK, kv_full, it.kvh, it.k0, it.bi, 128);
+        load_tile<DH>(sV, &tmV, kv_full, it.kvh, it.k0, it.bi, 128);
+        int hg = it.j0 / it.n, qi = it.j0 - hg * it.n;
+        for (int j = it.j0; j < it.j1; ++j, ++g) {
+          const int qs = static_cast<int>(g % kQdStages);
+          const uint32_t qph = static_cast<uint32_t>(g / kQdStages) & 1u;
+          if (!(ok = mbar_wait(&qd_empty[qs], qph ^ 1u, a.status, kStatusAttnTimeout))) break;
+          const int q0 = (it.i0 + qi) * kB64;
+          const int head = it.kvh * a.group + hg;
+          mbar_arrive_expect_tx(&qd_full[qs], 2 * kTile64 + 2 * kB64 * 4);
+          uint8_t* dst = sQdO + qs * (2 * kTile64);
+          load_tile<DH>(dst, &tmQ, &qd_full[qs], head, q0, it.bi, 64);
+          load_tile<DH>(dst + kTile64, &tmdO, &qd_full[qs], head, q0, it.bi, 64);
+          // The block's row terms; past sq they are zeros or the next row's
+          // values, which the mask never lets through.
+          const long long stat = (static_cast<long long>(it.bi) * a.heads + head) * a.sp + q0;
+          float* st_dst = s_stat + qs * (2 * kB64);
+          bulk_load(st_dst, a.nlse + stat, kB64 * 4, &qd_full[qs]);
+          bulk_load(st_dst + kB64, a.nd + stat, kB64 * 4, &qd_full[qs]);
+          if (++qi == it.n) {
+            qi = 0;
+            ++hg;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t kIdSP = idesc<BF>(128, 64, false, false);  // K Q^T, V dO^T
+      constexpr uint32_t kIdAcc = idesc<BF>(128, DH, false, true);  // P^T dO, dS^T Q
+      const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV);
+      // S^T / dP^T of ring position gg into buffer gg & 1, whose P^T / dS^T
+      // the products of position gg - 2 (issued before) have read.
+      auto issue_sp = [&](long long gg) -> bool {
+        const int st = static_cast<int>(gg & 1);
+        const int qs = static_cast<int>(gg % kQdStages);
+        if (!mbar_wait(&qd_full[qs], static_cast<uint32_t>(gg / kQdStages) & 1u, a.status,
+                       kStatusAttnTimeout))
+          return false;
+        tc_fence_after();
+        const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
+        const uint32_t do_addr = q_addr + kTile64;
+#pragma unroll
+        for (int kk = 0; kk < DH / 16; ++kk) {
+          umma_bf16(tS(st), sw128_desc(k_addr + k_off(kk, 128), 16, 1024),
+                    sw128_desc(q_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+          umma_bf16(tP(st), sw128_desc(v_addr + k_off(kk, 128), 16, 1024),
+                    sw128_desc(do_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[st]);
+        return true;
+      };
+      bool ok = true;
+      long long g = 0;  // query blocks of the items before this one
+      uint32_t it_no = 0;
+      for (int r = 0; ok; ++r) {
+        const int k = kv_item_index(r, a);
+        if (k < 0) break;
+        const KvItem it = kv_item(k, a);
+        const int len = it.j1 - it.j0;
+        if (len <= 0) continue;
+        if (!(ok = mbar_wait(kv_full, it_no & 1u, a.status, kStatusAttnTimeout))) break;
+        if (!(ok = issue_sp(g))) break;
+        if (len == 1) umma_commit(kv_empty);
+        for (int j = 0; j < len; ++j) {
+          const long long gj = g + j;
+          if (j + 1 < len) {
+            if (!(ok = issue_sp(gj + 1))) break;
+            if (j + 2 == len) umma_commit(kv_empty);  // the item's last S^T / dP^T
+          }
+          const int st = static_cast<int>(gj & 1);
+          if (!(ok = mbar_wait(&p_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+                               kStatusAttnTimeout)))
+            break;
+          // The item's first products overwrite the accumulators: the previous
+          // item's epilogue must have read them.
+          if (j == 0 && it_no > 0 &&
+              !(ok = mbar_wait(acc_empty, (it_no - 1u) & 1u, a.status, kStatusAttnTimeout)))
+            break;
+          tc_fence_after();
+          const int qs = static_cast<int>(gj % kQdStages);
+          const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
+          const uint32_t do_addr = q_addr + kTile64;
+#pragma unroll
+          for (int kk = 0; kk < kB64 / 16; ++kk) {
+            // queries [16 kk, 16 kk + 16): group kk / 2's columns, 8 columns each
+            const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
+            const uint32_t acc = (j | kk) != 0 ? 1u : 0u;
+            umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
+                        kIdAcc, acc);
+            umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
+                        kIdAcc, acc);
+          }
+          umma_commit(&qd_empty[qs]);
+        }
+        if (!ok) break;
+        umma_commit(acc_done);
+        g += len;
+        ++it_no;
+      }
+    }
+  } else if (warp >= 4) {
+    const int quarter = warp & 3;
+    const int grp = (warp - 4) >> 2;  // this warp's column half
+    const int c = grp * 32;
+    const int r = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+    bool ok = true;
+    long long gb = 0;  // query blocks of the items before this one
+    uint32_t it_no = 0;
+    for (int ri = 0; ok; ++ri) {
+      const int k = kv_item_index(ri, a);
+      if (k < 0) break;
+      const KvItem it = kv_item(k, a);
+      const int key = it.k0 + r;
+      const int len = it.j1 - it.j0;
+      // queries [qlo, qhi) see this key
+      const int qlo = key - a.off;
+      int qhi = a.sq;
+      if (key >= a.sinks)
+        qhi = static_cast<int>(min(static_cast<long long>(a.sq),
+                                   static_cast<long long>(key) + a.window - a.off));
+      if (key >= a.sk) qhi = 0;
+      int qi = it.n > 0 ? it.j0 % it.n : 0;
+      for (int j = 0; j < len; ++j) {
+        const long long gj = gb + j;
+        const int st = static_cast<int>(gj & 1);
+        const int qs = static_cast<int>(gj % kQdStages);
+        const int q0 = (it.i0 + qi) * kB64;
+        if (++qi == it.n) qi = 0;
+        if (!(ok = mbar_wait(&s_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+                             kStatusAttnTimeout)))
+          break;
+        // The block's row terms were staged with its Q / dO; the stage cannot
+        // be refilled before this block's products are done.
+        if (!(ok = mbar_wait(&qd_full[qs], static_cast<uint32_t>(gj / kQdStages) & 1u, a.status,
+                             kStatusAttnTimeout)))
+          break;
+        tc_fence_after();
+        const float* wstat = s_stat + qs * (2 * kB64) + c;
+        const int lo = qlo - q0 - c, hi = qhi - q0 - c;  // visible columns lo <= i < hi
+        float sv[32], pv[32];
+        tmem_ld32x2(tS(st) + lane_off + c, sv, tP(st) + lane_off + c, pv);
+        uint32_t pk[16], dk[16];
+        const bool full = lo <= 0 && hi >= 32;
+        const uint32_t vis = full ? 0xffffffffu : RowMask::prefix(hi) & ~RowMask::prefix(lo);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
+          const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+          const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
+          float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+          float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
+          if (!full) {
+            // hidden queries may stand on the row terms of another sequence
+            const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
+            p = make_float2(v0 ? p.x : 0.0f, v1 ? p.y : 0.0f);
+            d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
+          }
+          pk[i >> 1] = pack2<BF>(p.x, p.y);
+          const float2 g = __fmul2_rn(p, d);
+          dk[i >> 1] = pack2<BF>(g.x, g.y);
+        }
+        tmem_st16(tS(st) + lane_off + c, pk);  // P^T over this group's S^T columns
+        tmem_st16(tP(st) + lane_off + c, dk);  // dS^T over its dP^T columns
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[st]);
+      }
+      if (!ok) break;
+      if (len > 0) {
+        gb += len;
+        if (!(ok = mbar_wait(acc_done, it_no & 1u, a.status, kStatusAttnTimeout))) break;
+        ++it_no;
+        tc_fence_after();
+      }
+      const long long row = static_cast<long long>(it.bi) * a.sk + key;
+      uint8_t* okp = static_cast<uint8_t*>(a.dk) + (row * a.lddk + it.kvh * DH) * 2;
+      uint8_t* ovp = static_cast<uint8_t*>(a.dv) + (row * a.lddv + it.kvh * DH) * 2;
+      // partials: [slot][dK, dV][DH / 4][128 keys][4], so a warp's 32 rows
+      // store 512 contiguous bytes
+      float4* part = reinterpret_cast<float4*>(a.part) +
+                     static_cast<long long>(max(it.slot, 0)) * 2 * 128 * (DH / 4);
+#pragma unroll
+      for (int cc = grp * (DH / 2); cc < (grp + 1) * (DH / 2); cc += 32) {
+        float vk[32], vv[32];
+        if (len > 0) {
+          tmem_ld32(tdK + lane_off + cc, vk);
+          tmem_ld32(tdV + lane_off + cc, vv);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) vk[i] = vv[i] = 0.0f;
+        }
+        if (it.slot >= 0) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            part[(cc / 4 + q) * 128 + r] =
+                make_float4(vk[4 * q], vk[4 * q + 1], vk[4 * q + 2], vk[4 * q + 3]);
+            part[128 * (DH / 4) + (cc / 4 + q) * 128 + r] =
+                make_float4(vv[4 * q], vv[4 * q + 1], vv[4 * q + 2], vv[4 * q + 3]);
+          }
+        } else if (key < a.sk) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            *reinterpret_cast<uint4*>(okp + 2 * (cc + 8 * q)) = pack8t<BF>(vk + 8 * q, a.scale);
+            *reinterpret_cast<uint4*>(ovp + 2 * (cc + 8 * q)) = pack8t<BF>(vv + 8 * q, 1.0f);
+          }
+        }
+      }
+      if (len > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// Adds the slices of one cut key tile in slice order and writes dK (scaled)
+// and dV.  Block (tile slot group, 8 columns, dK or dV): thread = key row.
+template <bool BF, int DH>
+__global__ void __launch_bounds__(128) window_kv_join(const WinArgs a, int first_tile, int split,
+                                                      int slot0) {
+  const int bk = blockIdx.x % a.bkv, kb = blockIdx.x / a.bkv;  // kb: among the class's tiles
+  const int c8 = blockIdx.y, which = blockIdx.z;
+  const int kvh = bk % a.kv_heads, bi = bk / a.kv_heads;
+  const int key = (first_tile + kb) * kBN + threadIdx.x;
+  if (key >= a.sk) return;
+  const float4* p = reinterpret_cast<const float4*>(a.part) +
+                    (static_cast<long long>(slot0) + static_cast<long long>(kb * a.bkv + bk) * split) *
+                        (2 * 128 * (DH / 4)) +
+                    which * 128 * (DH / 4) + c8 * 2 * 128 + threadIdx.x;
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < split; ++s) {
+    const float4 x = __ldcg(p + static_cast<long long>(s) * 2 * 128 * (DH / 4));
+    const float4 y = __ldcg(p + static_cast<long long>(s) * 2 * 128 * (DH / 4) + 128);
+    v[0] += x.x;
+    v[1] += x.y;
+    v[2] += x.z;
+    v[3] += x.w;
+    v[4] += y.x;
+    v[5] += y.y;
+    v[6] += y.z;
+    v[7] += y.w;
+  }
+  const long long row = static_cast<long long>(bi) * a.sk + key;
+  uint8_t* out = which == 0
+                     ? static_cast<uint8_t*>(a.dk) + (row * a.lddk + kvh * DH + c8 * 8) * 2
+                     : static_cast<uint8_t*>(a.dv) + (row * a.lddv + kvh * DH + c8 * 8) * 2;
+  *reinterpret_cast<uint4*>(out) = pack8t<BF>(v, which == 0 ? a.scale : 1.0f);
+}
+
+// ------------------------------------------------------------------ host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn_win() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
+  }();
+  return fn;
+}
+
+// [seqs][rows][cols] two-byte matrix with row stride ld (elements); boxes of
+// 64 columns x box_rows rows of one sequence, 128-byte swizzle.
+bool make_map3(CUtensorMap* m, const void* ptr, bool bf, int64_t cols, int64_t rows, int64_t seqs,
+               int64_t ld, int box_rows) {
+  auto fn = encode_fn_win();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(seqs)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld * rows) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+            const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How the key tiles of the dK / dV kernel are cut.  A slice takes at least
+// kMinSlice blocks (about 1.1 us each; its partials cost 128 KB of traffic)
+// and about half of an SM's share of all blocks, so the items balance.
+constexpr int kMinSlice = 16;
+constexpr int kMaxSlices = 255;
+
+struct KvPlan {
+  int key_tiles, sink_tiles, split_s, split_w;
+  int64_t items, slots;
+};
+
+KvPlan plan_kv(const WindowAttn& w) {
+  KvPlan p{};
+  p.key_tiles = static_cast<int>((w.sk + kBN - 1) / kBN);
+  p.sink_tiles = static_cast<int>((w.sinks + kBN - 1) / kBN);
+  const int64_t bkv = w.b * w.kv_heads, group = w.heads / w.kv_heads;
+  int64_t blocks = 0, max_s = 0, max_w = 0;
+  for (int kb = 0; kb < p.key_tiles; ++kb) {
+    const int64_t n = group * query_blocks(kb * kBN, static_cast<int>(w.sq), static_cast<int>(w.sk),
+                                           static_cast<int>(w.window), static_cast<int>(w.sinks)).n;
+    blocks += n;
+    int64_t& mx = kb < p.sink_tiles ? max_s : max_w;
+    mx = std::max(mx, n);
+  }
+  const int64_t share = blocks * bkv / (2 * sm_count());
+  const int64_t slice = std::max<int64_t>(kMinSlice, share);
+  auto cut = [&](int64_t n) {
+    return static_cast<int>(std::min<int64_t>(kMaxSlices, std::max<int64_t>(1, (n + slice - 1) / slice)));
+  };
+  p.split_s = cut(max_s);
+  p.split_w = cut(max_w);
+  const int64_t ns = int64_t(p.sink_tiles) * bkv * p.split_s;
+  const int64_t nw = int64_t(p.key_tiles - p.sink_tiles) * bkv * p.split_w;
+  p.items = ns + nw;
+  p.slots = (p.split_s > 1 ? ns : 0) + (p.split_w > 1 ? nw : 0);
+  return p;
+}
+
+int64_t stat_stride(int64_t s) { return (s + 3) / 4 * 4; }
+
+size_t stat_bytes(const WindowAttn& w) {
+  const size_t n = static_cast<size_t>(w.b * w.heads) * stat_stride(w.sq) + 64;
+  return (n * sizeof(float) + 255) / 256 * 256;
+}
+
+WinArgs base_args(const WindowAttn& w) {
+  WinArgs a{};
+  a.sq = static_cast<int>(w.sq);
+  a.sk = static_cast<int>(w.sk);
+  a.off = a.sk - a.sq;
+  a.heads = w.heads;
+  a.kv_heads = w.kv_heads;
+  a.group = w.heads / w.kv_heads;
+  a.window = static_cast<int>(w.window);
+  a.sinks = static_cast<int>(w.sinks);
+  a.scale = w.scale;
+  a.scale_log2 = w.scale * kLog2e;
+  a.status = wait_ctl();
+  return a;
+}
+
+// Visible (query, key) pairs of all heads.
+double visible_pairs(const WindowAttn& w) {
+  double n = 0;
+  const double off = double(w.sk - w.sq);
+  // rows with p + 1 <= window see p + 1 keys, later ones window + sinks
+  const double p0 = std::max(0.0, off), p1 = double(w.sk);  // positions [p0, p1)
+  const double m = std::min(std::max(double(w.window), p0), p1);
+  n += (m * (m + 1) - p0 * (p0 + 1)) / 2;
+  n += (p1 - m) * double(std::min(w.window + w.sinks, w.sk));
+  return n * double(w.b) * w.heads;
+}
+
+template <typename K>
+tp_status smem_opt_in(K kern, int bytes, const char* what) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e == cudaSuccess ? TP_OK : cuda_fail(e, what);
+}
+
+template <bool BF, int DH>
+tp_status fwd(const WindowAttn& w, cudaStream_t stream) {
+  CUtensorMap q, k, v;
+  const int64_t nq = int64_t(w.heads) * DH, nk = int64_t(w.kv_heads) * DH;
+  if (!make_map3(&q, w.q, BF, nq, w.sq, w.b, w.ldq, 128) ||
+      !make_map3(&k, w.k, BF, nk, w.sk, w.b, w.ldk, 128) ||
+      !make_map3(&v, w.v, BF, nk, w.sk, w.b, w.ldv, 128))
+    return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (window attention)");
+  WinArgs a = base_args(w);
+  if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
+  a.o = const_cast<void*>(w.o);
+  a.ldo = w.ldo;
+  a.lse = const_cast<float*>(w.lse);
+  constexpr int smem = FwdSmem<DH>::kBytes;
+  if (tp_status s = smem_opt_in(window_fwd<BF, DH>, smem, "window attention smem"); s != TP_OK)
+    return s;
+  const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
+  dim3 grid(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
+  {
+    LaunchScope scope(TP_KIND_ATTN_FWD, 4.0 * DH * visible_pairs(w),
+                      4.0 * double(w.b) * (w.sq * nq + w.sk * nk), stream);
+    window_fwd<BF, DH><<<grid, kThreads, smem, stream>>>(q, k, v, a);
+  }
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TP_OK : cuda_fail(e, "window attention forward launch");
+}
+
+template <bool BF, int DH>
+tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
+  CUtensorMap q128, do128, k64, v64, k128, v128, q64, do64;
+  const int64_t nq = int64_t(w.heads) * DH, nk = int64_t(w.kv_heads) * DH;
+  if (!make_map3(&q128, w.q, BF, nq, w.sq, w.b, w.ldq, 128) ||
+      !make_map3(&do128, w.d_o, BF, nq, w.sq, w.b, w.lddo, 128) ||
+      !make_map3(&k64, w.k, BF, nk, w.sk, w.b, w.ldk, 64) ||
+      !make_map3(&v64, w.v, BF, nk, w.sk, w.b, w.ldv, 64) ||
+      !make_map3(&k128, w.k, BF, nk, w.sk, w.b, w.ldk, 128) ||
+      !make_map3(&v128, w.v, BF, nk, w.sk, w.b, w.ldv, 128) ||
+      !make_map3(&q64, w.q, BF, nq, w.sq, w.b, w.ldq, 64) ||
+      !make_map3(&do64, w.d_o, BF, nq, w.sq, w.b, w.lddo, 64))
+    return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (window attention backward)");
+  WinArgs a = base_args(w);
+  if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
+  const size_t sb = stat_bytes(w);
+  float* nlse = static_cast<float*>(scratch);
+  float* nd = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + sb);
+  a.nlse = nlse;
+  a.nd = nd;
+  a.sp = static_cast<int>(stat_stride(w.sq));
+  a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + 2 * sb);
+  a.dq = w.dq;
+  a.dk = w.dk;
+  a.dv = w.dv;
+  a.lddq = w.lddq;
+  a.lddk = w.lddk;
+  a.lddv = w.lddv;
+  const KvPlan p = plan_kv(w);
+  a.bkv = static_cast<int>(w.b * w.kv_heads);
+  a.key_tiles = p.key_tiles;
+  a.sink_tiles = p.sink_tiles;
+  a.split_s = p.split_s;
+  a.split_w = p.split_w;
+  a.items = static_cast<int>(p.items);
+  constexpr int smem_q = DqSmem<DH>::kBytes, smem_kv = KvSmem<DH>::kBytes;
+  if (tp_status s = smem_opt_in(window_bwd_dq<BF, DH>, smem_q, "window dQ smem"); s != TP_OK)
+    return s;
+  if (tp_status s = smem_opt_in(window_bwd_dkdv<BF, DH>, smem_kv, "window dK/dV smem"); s != TP_OK)
+    return s;
+  const int64_t rows = w.b * w.sq;
+  const int64_t pad = w.b * w.heads * (a.sp - w.sq) + 64;
+  const int64_t threads = std::max(rows * w.heads * (DH / 8), pad);
+  const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
+  dim3 gq(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
+  const unsigned gk = static_cast<unsigned>(std::min<int64_t>(p.items, sm_count()));
+  const int joins = (p.split_s > 1) + (p.split_w > 1 && p.key_tiles > p.sink_tiles);
+  LaunchScope scope(TP_KIND_ATTN_BWD, 10.0 * DH * visible_pairs(w),
+                    double(w.b) * (8.0 * w.sq * nq + 8.0 * w.sk * nk), stream, 3 + joins);
+  window_dsum<BF, DH><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
+      w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, rows, a.sq, a.heads, a.sp);
+  window_bwd_dq<BF, DH><<<gq, kThreads, smem_q, stream>>>(q128, do128, k64, v64, a);
+  window_bwd_dkdv<BF, DH><<<gk, kThreads, smem_kv, stream>>>(k128, v128, q64, do64, a);
+  if (p.split_s > 1)
+    window_kv_join<BF, DH><<<dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0, stream>>>(
+        a, 0, p.split_s, 0);
+  if (p.split_w > 1 && p.key_tiles > p.sink_tiles)
+    window_kv_join<BF, DH><<<dim3((p.key_tiles - p.sink_tiles) * a.bkv, DH / 8, 2), 128, 0,
+                             stream>>>(a, p.sink_tiles, p.split_w,
+                                       p.split_s > 1 ? p.sink_tiles * a.bkv * p.split_s : 0);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TP_OK : cuda_fail(e, "window attention backward launch");
+}
+
+}  // namespace
+
+tp_status window_attn_check(const WindowAttn& w) {
+  if ((w.sq + kBM - 1) / kBM > 65535 || w.b * w.heads > 0x7fffffffLL)
+    return fail(TP_ERR_SHAPE, "window attention: sequence or b * heads too large");
+  const int64_t tiles = (w.sk + kBN - 1) / kBN;
+  if (tiles * w.b * w.kv_heads > 0x7fffffffLL / kMaxSlices ||
+      (w.sq + kB64 - 1) / kB64 * (w.heads / w.kv_heads) > 0x7fffffffLL ||
+      w.b * w.sq * w.heads > (1ll << 34))
+    return fail(TP_ERR_SHAPE, "window attention: too many key tiles");
+  return TP_OK;
+}
+
+size_t window_attn_scratch_bytes(const WindowAttn& w) {
+  return 2 * stat_bytes(w) + static_cast<size_t>(plan_kv(w).slots) * 2 * kBN * w.d * 4;
+}
+
+tp_status launch_window_attn_fwd(const WindowAttn& w, cudaStream_t stream) {
+  if (w.dtype == TP_BF16)
+    return w.d == 64 ? fwd<true, 64>(w, stream) : fwd<true, 128>(w, stream);
+  return w.d == 64 ? fwd<false, 64>(w, stream) : fwd<false, 128>(w, stream);
+}
+
+tp_status launch_window_attn_bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
+  if (w.dtype == TP_BF16)
+    return w.d == 64 ? bwd<true, 64>(w, scratch, stream) : bwd<true, 128>(w, scratch, stream);
+  return w.d == 64 ? bwd<false, 64>(w, scratch, stream) : bwd<false, 128>(w, scratch, stream);
+}
+
+}  // namespace tp
