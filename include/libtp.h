@@ -88,8 +88,16 @@ typedef enum tp_op {
   TP_OP_BLOCK_BWD = 6,
   TP_OP_VOCAB_CE_FWD = 7,   /* f is the vocabulary size V */
   TP_OP_VOCAB_EMBED_BWD = 8, /* depends on M only */
-  TP_OP_QK_NORM_ROPE_BWD = 9 /* h is the head dimension d; depends on d only */
+  TP_OP_QK_NORM_ROPE_BWD = 9, /* h is the head dimension d; depends on d only */
+  TP_OP_GLU_FWD = 10,
+  TP_OP_GLU_BWD = 11
 } tp_op;
+
+/* Activation of the gate in tp_glu_fwd / tp_glu_bwd. */
+typedef enum tp_act {
+  TP_ACT_SILU = 0, /* x / (1 + exp(-x))                     */
+  TP_ACT_GELU = 1  /* the erf GeLU, evaluated as tp_mlp_fwd */
+} tp_act;
 
 /*
  * Column-parallel linear ([P3] §1.2; [P2] §3.2 ColumnParallelLinear):
@@ -393,6 +401,43 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
                           const void* logits, const float* lse, const float* dloss,
                           void* dlogits, void* dX, void* dE, int64_t M, int64_t h, int64_t V,
                           int t, tp_dtype dtype, void* stream);
+
+/*
+ * Partitioned gated feed-forward block, bf16:
+ *   G = X Wg + bg,  U = X Wu + bu,  H = act(G) * U,  Z = H Wd + bd.
+ * Wgu [h, 2f] = [Wg | Wu]; Wgu is split by columns (shard i owns columns
+ * [i f/t, (i+1) f/t) of both halves), Wd by rows, as in tp_mlp_fwd: both
+ * projections, the activation and the product are one kernel, and the shards'
+ * products with Wd are summed in its accumulator.
+ *   X [M, h]; bgu [2f] = [bg | bu] or NULL; Wd [f, h]; bd [h] or NULL;
+ *   Z [M, h]; GUsave [M, 2f] = [G | U] (rounded to bf16) or NULL: kept for
+ *   the backward.  H is rounded to bf16 and lives in the workspace.
+ *   Up to 64 tokens take kernels that stream the weights once (a token's
+ *   cost is reading them); their sums are grouped differently from the
+ *   larger batches'.
+ * Errors: NULL X / Wgu / Wd / Z; f % t; alignment (h, f multiples of 8);
+ *   dtype must be TP_BF16 (else TP_ERR_UNSUPPORTED); act unknown
+ *   (TP_ERR_UNSUPPORTED); TP_ERR_WORKSPACE.
+ */
+tp_status tp_glu_fwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,
+                     const void* bd, void* Z, void* GUsave, int64_t M, int64_t h, int64_t f, int t,
+                     tp_act act, tp_dtype dtype, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of tp_glu_fwd, the mirror rule per shard:
+ *   dH = dZ Wd^T;  dG = dH * U * act'(G);  dU = dH * act(G);
+ *   dWd = H^T dZ;  dWgu = X^T [dG | dU];  dX = [dG | dU] Wgu^T (the shards'
+ *   and both halves' partials summed in the accumulator);
+ *   dbgu = colsum([dG | dU]);  dbd = colsum(dZ).
+ *   GUsave: from the forward, or NULL to recompute it from X, Wgu, bgu.
+ *   Outputs dX [M, h], dWgu [h, 2f], dWd [f, h], and dbgu [2f], dbd [h] when
+ *   not NULL; all bf16.  Deterministic.
+ * Errors: as tp_glu_fwd; NULL dZ / dX / dWgu / dWd.
+ */
+tp_status tp_glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,
+                     const void* GUsave, const void* dZ, void* dX, void* dWgu, void* dbgu,
+                     void* dWd, void* dbd, int64_t M, int64_t h, int64_t f, int t, tp_act act,
+                     tp_dtype dtype, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * RMS norm of every query and key head with the rotary position in the same

@@ -22,7 +22,8 @@ TP_ERR_UNSUPPORTED, TP_ERR_CUDA, TP_ERR_KERNEL, TP_ERR_WORKSPACE = 5, 6, 7, 8
 TP_F32, TP_BF16, TP_F16 = 0, 1, 2
 TP_OP_MLP_FWD, TP_OP_MLP_BWD, TP_OP_ATTN_FWD, TP_OP_ATTN_BWD = 0, 1, 2, 3
 TP_OP_LN_BWD, TP_OP_BLOCK_FWD, TP_OP_BLOCK_BWD, TP_OP_VOCAB_CE_FWD = 4, 5, 6, 7
-TP_OP_VOCAB_EMBED_BWD, TP_OP_QK_NORM_ROPE_BWD = 8, 9
+TP_OP_VOCAB_EMBED_BWD, TP_OP_QK_NORM_ROPE_BWD, TP_OP_GLU_FWD, TP_OP_GLU_BWD = 8, 9, 10, 11
+TP_ACT_SILU, TP_ACT_GELU = 0, 1
 
 (TP_KIND_GEMM_TCGEN05, TP_KIND_GEMM_SIMT, TP_KIND_ATTN_FWD, TP_KIND_ATTN_BWD, TP_KIND_REDUCE,
  TP_KIND_VOCAB) = range(6)
@@ -38,7 +39,7 @@ EXPORTS = ("tp_linear_col", "tp_linear_row", "tp_mlp_fwd", "tp_mlp_bwd", "tp_att
            "tp_vocab_embed_bwd", "tp_vocab_ce_fwd", "tp_vocab_ce_bwd", "tp_gemm_plan",
            "tp_selftest_bounded_wait", "tp_qk_norm_rope_fwd", "tp_qk_norm_rope_bwd",
            "tp_window_attn_fwd", "tp_window_attn_bwd", "tp_window_attn_workspace_size",
-           "tp_window_attn_decode", "tp_window_decode_workspace_size")
+           "tp_window_attn_decode", "tp_window_decode_workspace_size", "tp_glu_fwd", "tp_glu_bwd")
 
 _W_FIELDS = ("ln1_g", "ln1_b", "Wqkv", "Wo", "ln2_g", "ln2_b", "A", "bA", "B", "bB")
 _S_FIELDS = ("Xn1", "mean1", "rstd1", "QKV", "O", "LSE", "X1", "Xn2", "mean2", "rstd2", "Y")
@@ -120,6 +121,9 @@ def load() -> ctypes.CDLL:
     L.tp_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, i64,
                                       vp, i64, vp, vp, i64, i32, i32, i32, i32, i32, i32, f32, i32,
                                       vp, sz, vp]
+    L.tp_glu_fwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, vp, sz, vp]
+    L.tp_glu_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
+                             i32, vp, sz, vp]
     L.tp_window_attn_fwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, i32,
                                      i32, i32, i64, i64, f32, i32, vp]
     L.tp_window_attn_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, vp,
@@ -422,6 +426,42 @@ def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk,
 def qk_norm_rope_workspace(M: int, d: int, device="cuda") -> torch.Tensor:
     """Workspace of tp_qk_norm_rope_bwd."""
     return workspace(TP_OP_QK_NORM_ROPE_BWD, M, d, 0, 0, 1, TP_BF16, device)
+
+
+def _glu_sizes(X, Wgu, Wd, tensors):
+    M, h = X.shape
+    f = Wd.shape[0]
+    if Wgu.shape != (h, 2 * f) or Wd.shape[1] != h:
+        raise ValueError("X [M, h], Wgu [h, 2 f] and Wd [f, h] are required")
+    for t, shape, n in ((Wgu, (h, 2 * f), "Wgu"), (Wd, (f, h), "Wd")) + tensors(M, h, f):
+        if t is not None and (t.numel() != torch.Size(shape).numel() or t.dtype != X.dtype
+                              or t.device != X.device):
+            raise ValueError(f"{n}: {shape} of {X.dtype} on {X.device} is required")
+    return M, h, f
+
+
+def tp_glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, t: int, act: int, ws, stream=None) -> None:
+    """Z = (act(X Wg + bg) * (X Wu + bu)) Wd + bd with Wgu = [Wg | Wu] [h, 2 f];
+    GUsave [M, 2 f] (or None) keeps [G | U] for the backward."""
+    M, h, f = _glu_sizes(X, Wgu, Wd, lambda M, h, f: (
+        (bgu, (2 * f,), "bgu"), (bd, (h,), "bd"), (Z, (M, h), "Z"), (GUsave, (M, 2 * f), "GUsave")))
+    with _on(X, stream) as st:
+        _check(load().tp_glu_fwd(_ptr(X), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(bd), _ptr(Z),
+                                 _ptr(GUsave), M, h, f, t, act, _dtype(X), _ptr(ws),
+                                 ws.numel() * ws.element_size(), st))
+
+
+def tp_glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t: int, act: int, ws,
+               stream=None) -> None:
+    """Backward of tp_glu_fwd; GUsave None recomputes [G | U]; dbgu, dbd may be None."""
+    M, h, f = _glu_sizes(X, Wgu, Wd, lambda M, h, f: (
+        (bgu, (2 * f,), "bgu"), (GUsave, (M, 2 * f), "GUsave"), (dZ, (M, h), "dZ"),
+        (dX, (M, h), "dX"), (dWgu, (h, 2 * f), "dWgu"), (dbgu, (2 * f,), "dbgu"),
+        (dWd, (f, h), "dWd"), (dbd, (h,), "dbd")))
+    with _on(X, stream) as st:
+        _check(load().tp_glu_bwd(_ptr(X), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(GUsave), _ptr(dZ),
+                                 _ptr(dX), _ptr(dWgu), _ptr(dbgu), _ptr(dWd), _ptr(dbd), M, h, f, t,
+                                 act, _dtype(X), _ptr(ws), ws.numel() * ws.element_size(), st))
 
 
 def _heads(x, n: int, what: str) -> int:

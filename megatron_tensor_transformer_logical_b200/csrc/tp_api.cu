@@ -891,6 +891,150 @@ tp_status vocab_ce_bwd(const void* X, const void* E, const int32_t* targets, con
   return TP_OK;
 }
 
+// ------------------------------------------------ gated feed-forward block
+
+size_t glu_fwd_ws_min(int64_t M, int64_t f) { return align_up(M * f * 2, 256) + 256; }
+
+size_t glu_bwd_colsum_bytes(int64_t M, int64_t h, int64_t f) {
+  return align_up(dba_partial_bytes(M, 2 * f), 256) + mlp_bias_grads_scratch_bytes(M, h);
+}
+
+size_t glu_bwd_ws_min(int64_t M, int64_t h, int64_t f) {
+  // [dG | dU], H, the recomputed [G | U], column sums
+  return 5 * align_up(M * f * 2, 256) + align_up(glu_bwd_colsum_bytes(M, h, f), 256) + 2048;
+}
+
+tp_status glu_check(int64_t M, int64_t h, int64_t f, int t, tp_act act, tp_dtype dtype) {
+  TP_TRY(check_dtype(dtype));
+  if (dtype != TP_BF16) return fail(TP_ERR_UNSUPPORTED, "the gated block is implemented for bf16 only");
+  if (act != TP_ACT_SILU && act != TP_ACT_GELU) return fail(TP_ERR_UNSUPPORTED, "unknown activation");
+  if (M <= 0 || h <= 0 || f <= 0) return fail(TP_ERR_SHAPE, "M, h and f must be positive");
+  if (f > kMaxDim / 2 || !dims_ok({M, h, 2 * f}))
+    return fail(TP_ERR_SHAPE, "M, h and 2 f must be below 2^31 - 256");
+  TP_TRY(check_t(t));
+  if (f % t != 0) return fail(TP_ERR_SHAPE, "f must be divisible by t");
+  return check_rows({h, f});
+}
+
+// H = act(X Wg + bg) * (X Wu + bu), [G | U] to GU unless nullptr.
+tp_status glu_up(const void* X, const void* Wgu, const void* bgu, void* H, void* GU, int64_t M,
+                 int64_t h, int64_t f, int t, tp_act act, const Tail& tail, cudaStream_t stream) {
+  Gemm g;
+  g.M = M; g.N = f; g.K = h;
+  g.a = {X, h, true};
+  g.b = {Wgu, 2 * f, false};
+  g.epi = kEpiGlu;
+  g.act = act;
+  g.out = H; g.ldo = f;
+  g.bias = bgu;
+  g.out2 = GU; g.ldo2 = 2 * f;
+  g.n_shard = f / t;
+  tail.to(g);
+  return launch_gemm_bf16(g, stream);
+}
+
+tp_status glu_fwd(const void* X, const void* Wgu, const void* bgu, const void* Wd, const void* bd,
+                  void* Z, void* GUsave, int64_t M, int64_t h, int64_t f, int t, tp_act act,
+                  tp_dtype dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!X || !Wgu || !Wd || !Z) return fail(TP_ERR_NULL, "X, Wgu, Wd and Z are required");
+  TP_TRY(glu_check(M, h, f, t, act, dtype));
+  TP_TRY(check_ptrs_aligned({X, Wgu, bgu, Wd, bd, Z, GUsave, ws}));
+  if (ws == nullptr || ws_bytes < glu_fwd_ws_min(M, f))
+    return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_workspace_size()");
+  Carve c(ws, ws_bytes);
+  void* H = c.take(M * f * 2);
+  if (M <= kThinMaxM) {
+    ThinGlu g;
+    g.x = X; g.wgu = Wgu; g.bgu = bgu; g.wd = Wd; g.bd = bd;
+    g.H = H; g.gu = GUsave; g.z = Z;
+    g.M = M; g.h = h; g.f = f;
+    g.act = act;
+    return launch_thin_glu(g, stream);
+  }
+  const Tail tail(c);
+  TP_TRY(glu_up(X, Wgu, bgu, H, GUsave, M, h, f, t, act, tail, stream));
+  // Row-split second linear: the shards' products are summed in the accumulator.
+  Gemm g2;
+  g2.M = M; g2.N = h; g2.K = f;
+  g2.a = {H, f, true};
+  g2.b = {Wd, h, false};
+  g2.out = Z; g2.ldo = h;
+  g2.bias = bd;
+  tail.to(g2);
+  return launch_gemm_bf16(g2, stream);
+}
+
+tp_status glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,
+                  const void* GUsave, const void* dZ, void* dX, void* dWgu, void* dbgu, void* dWd,
+                  void* dbd, int64_t M, int64_t h, int64_t f, int t, tp_act act, tp_dtype dtype,
+                  void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!X || !Wgu || !Wd || !dZ || !dX || !dWgu || !dWd)
+    return fail(TP_ERR_NULL, "X, Wgu, Wd, dZ, dX, dWgu and dWd are required");
+  TP_TRY(glu_check(M, h, f, t, act, dtype));
+  TP_TRY(check_ptrs_aligned({X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, ws}));
+  if (ws == nullptr || ws_bytes < glu_bwd_ws_min(M, h, f))
+    return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_workspace_size()");
+  Carve c(ws, ws_bytes);
+  void* dGU = c.take(M * 2 * f * 2);
+  void* H = c.take(M * f * 2);
+  void* GUrec = c.take(M * 2 * f * 2);
+  void* scratch = c.take(glu_bwd_colsum_bytes(M, h, f));
+  const Tail tail(c);
+
+  const void* GU = GUsave;
+  if (GU == nullptr) {
+    TP_TRY(glu_up(X, Wgu, bgu, H, GUrec, M, h, f, t, act, tail, stream));
+    GU = GUrec;
+  }
+  // dH_i = dZ Wd_i^T per column shard; the epilogue turns it into [dG | dU]
+  // and rebuilds H (already there when recomputed).
+  Gemm g1;
+  g1.M = M; g1.N = f; g1.K = h;
+  g1.a = {dZ, h, true};
+  g1.b = {Wd, h, true};  // Wd [f, h] read as Wd^T: n = f index, K contiguous
+  g1.epi = kEpiDGlu;
+  g1.act = act;
+  g1.aux = GU; g1.ldaux = 2 * f;
+  g1.out = dGU; g1.ldo = 2 * f;
+  g1.out2 = GUsave != nullptr ? H : nullptr; g1.ldo2 = f;
+  g1.n_shard = f / t;
+  if (dbgu != nullptr) g1.csum_part = static_cast<float*>(scratch);
+  tail.to(g1);
+  TP_TRY(launch_gemm_bf16(g1, stream));
+
+  // dWd_i = H_i^T dZ: shard i's rows of dWd.
+  Gemm g2;
+  g2.M = f; g2.N = h; g2.K = M;
+  g2.a = {H, f, false};
+  g2.b = {dZ, h, false};
+  g2.out = dWd; g2.ldo = h;
+  tail.to(g2);
+  TP_TRY(launch_gemm_bf16(g2, stream));
+
+  // dWgu = X^T [dG | dU]: shard i's columns of both halves.
+  Gemm g3;
+  g3.M = h; g3.N = 2 * f; g3.K = M;
+  g3.a = {X, h, false};
+  g3.b = {dGU, 2 * f, false};
+  g3.out = dWgu; g3.ldo = 2 * f;
+  g3.n_shard = f / t;
+  tail.to(g3);
+  TP_TRY(launch_gemm_bf16(g3, stream));
+
+  // dX = [dG | dU] Wgu^T: both halves and all shards in one accumulator.
+  Gemm g4;
+  g4.M = M; g4.N = h; g4.K = 2 * f;
+  g4.a = {dGU, 2 * f, true};
+  g4.b = {Wgu, 2 * f, true};  // Wgu [h, 2f] read as Wgu^T
+  g4.out = dX; g4.ldo = h;
+  tail.to(g4);
+  TP_TRY(launch_gemm_bf16(g4, stream));
+
+  return launch_mlp_bias_grads(
+      dZ, M, h, dbd, static_cast<const float*>(scratch), 2 * f, dbgu,
+      static_cast<char*>(scratch) + align_up(dba_partial_bytes(M, 2 * f), 256), stream);
+}
+
 // ------------------------------------------- query / key norm + rotary
 
 tp_status check_half_dtype(tp_dtype d) {
@@ -1171,6 +1315,21 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
                                dtype, static_cast<cudaStream_t>(stream));)
 }
 
+tp_status tp_glu_fwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,
+                     const void* bd, void* Z, void* GUsave, int64_t M, int64_t h, int64_t f, int t,
+                     tp_act act, tp_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  TP_GUARD(return glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, M, h, f, t, act, dtype, ws, ws_bytes,
+                          static_cast<cudaStream_t>(stream));)
+}
+
+tp_status tp_glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,
+                     const void* GUsave, const void* dZ, void* dX, void* dWgu, void* dbgu,
+                     void* dWd, void* dbd, int64_t M, int64_t h, int64_t f, int t, tp_act act,
+                     tp_dtype dtype, void* ws, size_t ws_bytes, void* stream) {
+  TP_GUARD(return glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, M, h, f, t, act,
+                          dtype, ws, ws_bytes, static_cast<cudaStream_t>(stream));)
+}
+
 tp_status tp_qk_norm_rope_fwd(const void* Q, int64_t ldq, const void* K, int64_t ldk,
                               const void* gq, const void* gk, const int32_t* pos,
                               const double* inv_freq, void* Qo, int64_t ldqo, void* Ko,
@@ -1293,6 +1452,10 @@ size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, i
       case TP_OP_BLOCK_BWD: return (heads > 0 && f > 0) ? block_bwd_ws(M, h, f, heads) : 0;
       case TP_OP_VOCAB_CE_FWD: return (f > 0 && f % t == 0) ? ce_fwd_ws(M, f, t) : 0;
       case TP_OP_VOCAB_EMBED_BWD: return embed_bwd_ws(M);
+      case TP_OP_GLU_FWD:
+      case TP_OP_GLU_BWD:
+        if (f <= 0 || f > kMaxDim / 2 || dtype != TP_BF16) return 0;
+        return (op == TP_OP_GLU_FWD ? glu_fwd_ws_min(M, f) : glu_bwd_ws_min(M, h, f)) + tail_ws();
       case TP_OP_QK_NORM_ROPE_BWD: break;  // answered above
     }
   } catch (...) {

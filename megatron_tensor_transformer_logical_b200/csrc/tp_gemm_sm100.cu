@@ -43,6 +43,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "epi_math.cuh"
 #include "ptx_sm100.cuh"
 #include "tp_internal.h"
 
@@ -87,8 +88,9 @@ template <int BN, int EPI>
 struct Layout {
   static constexpr bool kAux = (EPI == kEpiResidual || EPI == kEpiDGelu);
   static constexpr bool kOut2 = (EPI == kEpiBiasGelu || EPI == kEpiDGelu);
+  static constexpr bool kGlu = (EPI == kEpiGlu || EPI == kEpiDGlu);  // two boxes in turn
   static constexpr bool kAhead = BN == 192 && kAux;
-  static constexpr bool kOneBox = BN == 192 && !kAux && !kOut2;
+  static constexpr bool kOneBox = BN == 192 && !kAux && !kOut2 && !kGlu;
   static constexpr int kStages = kOneBox ? 5 : Cfg<BN>::kStages;
   static constexpr int kBoxes = kOneBox ? 1 : 2;  // output boxes per epilogue warp
   static constexpr int kBoxBytes = kEpiWarps * kBoxes * kEpiBoxBytes;
@@ -128,7 +130,8 @@ struct Args {
   // Whole 32-column chunks of a two-byte output go through the shared-memory
   // boxes and the tensor maps tmO (out), tmO2 (out2) and tmX (aux).
   int tma_out;
-  // kEpiDGelu only: column sums of the output (fp32, before rounding) per
+  int act;  // kEpiGlu / kEpiDGlu: the activation (tp_act)
+  // kEpiDGelu / kEpiDGlu only: column sums of the output (fp32, before rounding) per
   // 32-row group, csum_part[(row / 32) * csum_ld + col]; nullptr: none.
   float* csum_part;
   long long csum_ld;
@@ -177,6 +180,11 @@ struct TileCoord {
   int m0, n0, n_end;
 };
 
+// Output columns of a tile with BN accumulator columns: the gated epilogue
+// forms one from a gate and an up column (the accumulator holds BN / 2 of each).
+template <int BN, int EPI>
+constexpr int kTileW = EPI == kEpiGlu ? BN / 2 : BN;
+
 // Grouped raster: bands of group_m row tiles; inside a band the row tile
 // varies fastest, so the CTAs running at one time share B tiles and the
 // band's A rows stay in L2.
@@ -212,89 +220,6 @@ __device__ __forceinline__ int k_coord(int kb, const Args& a) {
   return which * a.kr_h + g * a.kr_width + within * BK;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// The standard normal distribution at x: Phi(x) = (1 + erf(x / sqrt 2)) / 2
-// and phi(x) = exp(-x^2 / 2) / sqrt(2 pi), with erf by Abramowitz & Stegun,
-// "Handbook of Mathematical Functions", formula 7.1.26: for z >= 0,
-// erf z = 1 - t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) exp(-z^2),
-// t = 1 / (1 + p z), |error| <= 1.5e-7, and erf(-z) = -erf z.  With
-// z = |x| / sqrt 2 the factor exp(-z^2) is the exp(-x^2 / 2) of phi, so one
-// reciprocal and one exponential give both.  GeLU(x) = x Phi(x) (the erf
-// form) and GeLU'(x) = Phi(x) + x phi(x).  Two values at a time, on sm_100's
-// two-wide fp32 instructions (each lane rounded as the one-wide form): on
-// short-K GEMMs the epilogue's instruction issue, not the tensor core, sets
-// the pace.
-__device__ __forceinline__ float2 f2(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ void normal_cdf_pdf2(float2 x, float2& cdf, float2& pdf) {
-  const float2 z = __fmul2_rn(make_float2(fabsf(x.x), fabsf(x.y)), f2(0.70710678118654752f));
-  const float2 d = __ffma2_rn(f2(0.3275911f), z, f2(1.0f));
-  const float2 t = make_float2(rcp_approx(d.x), rcp_approx(d.y));
-  float2 p = __ffma2_rn(t, f2(1.061405429f), f2(-1.453152027f));
-  p = __ffma2_rn(t, p, f2(1.421413741f));
-  p = __ffma2_rn(t, p, f2(-0.284496736f));
-  p = __ffma2_rn(t, p, f2(0.254829592f));
-  const float2 poly = __fmul2_rn(t, p);
-  const float2 arg = __fmul2_rn(__fmul2_rn(x, f2(-0.5f * kLog2e)), x);
-  const float2 e = make_float2(ex2_approx(arg.x), ex2_approx(arg.y));  // exp(-x^2 / 2)
-  const float2 q = __fmul2_rn(__fmul2_rn(f2(0.5f), poly), e);         // (1 - erf z) / 2
-  const float2 r = __fadd2_rn(f2(1.0f), make_float2(-q.x, -q.y));
-  cdf = make_float2(x.x >= 0.0f ? r.x : q.x, x.y >= 0.0f ? r.y : q.y);
-  pdf = __fmul2_rn(f2(0.39894228040143268f), e);
-}
-
-// GeLU on eight values, in pairs.
-__device__ __forceinline__ void gelu8(float* x) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 v = make_float2(x[i], x[i + 1]);
-    float2 cdf, pdf;
-    normal_cdf_pdf2(v, cdf, pdf);
-    const float2 g = __fmul2_rn(v, cdf);
-    x[i] = g.x;
-    x[i + 1] = g.y;
-  }
-}
-
-// x *= GeLU'(y) on eight values, in pairs; with hh, also hh = GeLU(y).
-__device__ __forceinline__ void dgelu8(float* x, const float* y, float* hh) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 v = make_float2(y[i], y[i + 1]);
-    float2 cdf, pdf;
-    normal_cdf_pdf2(v, cdf, pdf);
-    if (hh != nullptr) {
-      const float2 g = __fmul2_rn(v, cdf);
-      hh[i] = g.x;
-      hh[i + 1] = g.y;
-    }
-    const float2 r = __fmul2_rn(make_float2(x[i], x[i + 1]), __ffma2_rn(v, pdf, cdf));
-    x[i] = r.x;
-    x[i + 1] = r.y;
-  }
-}
-
-// x += b on eight values, in pairs.
-__device__ __forceinline__ void add8(float* x, const float* b) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 r = __fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(b[i], b[i + 1]));
-    x[i] = r.x;
-    x[i + 1] = r.y;
-  }
-}
-
-__device__ __forceinline__ void unpack8(const uint4& u, float* f) {
-  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(p[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
-}
-
 // Output element types of the epilogue.
 enum Out : int { kOutBF16 = 0, kOutF32 = 1, kOutF16 = 2 };
 
@@ -315,17 +240,6 @@ __device__ __forceinline__ uint4 pack8_f16(float* f, bool& clamped) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-    w[i] = *reinterpret_cast<uint32_t*>(&t);
-  }
-  return u;
-}
-
-__device__ __forceinline__ uint4 pack8(const float* f) {
-  uint4 u;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    __nv_bfloat162 t = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
     w[i] = *reinterpret_cast<uint32_t*>(&t);
   }
   return u;
@@ -426,6 +340,84 @@ __device__ __forceinline__ void epilogue_colsum(float (&v)[32], int row, int col
     if (col0 + lane < col_end)
       a.csum_part[static_cast<long long>(row >> 5) * a.csum_ld + col0 + lane] = sum;
   }
+}
+
+// Adds a warp's 32-row column sums of one half of a gated gradient to the
+// partials (rows past M and columns past col_end count as zero).  Destroys v.
+__device__ __forceinline__ void glu_colsum(float (&v)[32], int row, int ncols, int pcol0, int lane,
+                                           const Args& a) {
+  if (row >= a.M) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+  }
+  const float sum = warp_colsum32(v, lane);
+  if (lane < ncols)
+    a.csum_part[static_cast<long long>(row >> 5) * a.csum_ld + pcol0 + lane] = sum;
+}
+
+// kEpiGlu on 32 columns of one row with direct stores: g, u the two products.
+__device__ __forceinline__ void epilogue_glu_row32(float (&g)[32], float (&u)[32], int row,
+                                                   int col0, int col_end, const Args& a) {
+  if (row >= a.M) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int col = col0 + 8 * q;
+    if (col + 8 > col_end) continue;
+    float *x = g + 8 * q, *y = u + 8 * q;
+    if (a.bias != nullptr) {
+      const __nv_bfloat16* bp = static_cast<const __nv_bfloat16*>(a.bias);
+      float bb[8];
+      unpack8(*reinterpret_cast<const uint4*>(bp + col), bb);
+      add8(x, bb);
+      unpack8(*reinterpret_cast<const uint4*>(bp + a.N + col), bb);
+      add8(y, bb);
+    }
+    if (a.out2 != nullptr) {
+      __nv_bfloat16* o2 = a.out2 + (long long)row * a.ldo2 + col;
+      *reinterpret_cast<uint4*>(o2) = pack8(x);
+      *reinterpret_cast<uint4*>(o2 + a.N) = pack8(y);
+    }
+    float h[8];
+    gate_act8(x, a.act, h, nullptr);
+    mul8(h, y);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + col) =
+        pack8(h);
+  }
+}
+
+// kEpiDGlu on 32 columns of one row with direct loads and stores; leaves dg
+// in v and du in du.
+__device__ __forceinline__ void epilogue_dglu_row32(float (&v)[32], float (&du)[32], int row,
+                                                    int col0, int col_end, const Args& a) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int col = col0 + 8 * q;
+    float *x = v + 8 * q, *y = du + 8 * q;
+    if (row >= a.M || col + 8 > col_end) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
+      continue;
+    }
+    const __nv_bfloat16* gp = a.aux + (long long)row * a.ldaux + col;
+    float g[8], u[8], h[8];
+    unpack8(*reinterpret_cast<const uint4*>(gp), g);
+    unpack8(*reinterpret_cast<const uint4*>(gp + a.N), u);
+    dglu8(x, g, u, a.act, y, h);
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + col;
+    *reinterpret_cast<uint4*>(o) = pack8(x);
+    *reinterpret_cast<uint4*>(o + a.N) = pack8(y);
+    if (a.out2 != nullptr)
+      *reinterpret_cast<uint4*>(a.out2 + (long long)row * a.ldo2 + col) = pack8(h);
+  }
+}
+
+// The bias gradient [dbg | dbu] of a kEpiDGlu epilogue's 32 columns.
+__device__ __forceinline__ void epilogue_glu_colsum(float (&dg)[32], float (&du)[32], int row,
+                                                    int col0, int col_end, int lane,
+                                                    const Args& a) {
+  if (a.csum_part == nullptr) return;
+  glu_colsum(dg, row, col_end - col0, col0, lane, a);
+  glu_colsum(du, row, col_end - col0, a.N + col0, lane, a);
 }
 
 // Byte offset of 16-byte chunk j (0-3) of row r in a 32-row x 64-byte box
@@ -624,6 +616,138 @@ __device__ __forceinline__ bool epilogue_chunk_ahead(uint32_t taddr, int lane, i
   return true;
 }
 
+// Hands the warp's boxes to TMA stores (issued by `store` on lane 0) and, if
+// they are to be written again, waits until they have been read.
+template <typename F>
+__device__ __forceinline__ void box_flush(int lane, bool reuse, F store) {
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    store();
+    bulk_commit();
+    if (reuse) bulk_wait_read<0>();
+  }
+  if (reuse) __syncwarp();
+}
+
+// kEpiGlu on a whole 32-column chunk through the warp's two boxes: g and u
+// leave first (when they are kept), then h through the first box.  tg, tu:
+// tensor-memory addresses of the two products; bg, bu: the biases of the
+// warp's half tile (bias_half), this chunk's from lane bl0 on.
+__device__ __forceinline__ void epilogue_glu_boxed(uint32_t tg, uint32_t tu, int lane, int row0,
+                                                   int col, uint8_t* box0, uint8_t* box1,
+                                                   const CUtensorMap* tmO, const CUtensorMap* tmO2,
+                                                   const uint4& bg, const uint4& bu, int bl0,
+                                                   const Args& a) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+  float g[32], u[32];
+  tmem_ld32(tg, g);
+  tmem_ld32(tu, u);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float *x = g + 8 * q, *y = u + 8 * q;
+    if (a.bias != nullptr) {
+      float bb[8];
+      unpack8(make_uint4(__shfl_sync(0xffffffffu, bg.x, bl0 + q),
+                         __shfl_sync(0xffffffffu, bg.y, bl0 + q),
+                         __shfl_sync(0xffffffffu, bg.z, bl0 + q),
+                         __shfl_sync(0xffffffffu, bg.w, bl0 + q)), bb);
+      add8(x, bb);
+      unpack8(make_uint4(__shfl_sync(0xffffffffu, bu.x, bl0 + q),
+                         __shfl_sync(0xffffffffu, bu.y, bl0 + q),
+                         __shfl_sync(0xffffffffu, bu.z, bl0 + q),
+                         __shfl_sync(0xffffffffu, bu.w, bl0 + q)), bb);
+      add8(y, bb);
+    }
+    if (a.out2 != nullptr) {
+      *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)) = pack8(x);
+      *reinterpret_cast<uint4*>(box1 + sw64_off(lane, q)) = pack8(y);
+    }
+  }
+  if (a.out2 != nullptr)
+    box_flush(lane, true, [&] {
+      tma_store_2d(tmO2, box0, col, row0);
+      tma_store_2d(tmO2, box1, a.N + col, row0);
+    });
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float h[8];
+    gate_act8(g + 8 * q, a.act, h, nullptr);
+    mul8(h, u + 8 * q);
+    *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)) = pack8(h);
+  }
+  box_flush(lane, false, [&] { tma_store_2d(tmO, box0, col, row0); });
+}
+
+// kEpiDGlu on a whole 32-column chunk: g and u arrive in the two boxes (TMA),
+// dg and du leave through them, then h through the first.  Returns false if
+// the wait for g and u gave up.
+__device__ __forceinline__ bool epilogue_dglu_boxed(uint32_t taddr, int lane, int row, int row0,
+                                                    int col, int col_end, uint8_t* box0,
+                                                    uint8_t* box1, uint64_t* auxbar,
+                                                    uint32_t& aux_phase, const CUtensorMap* tmO,
+                                                    const CUtensorMap* tmO2,
+                                                    const CUtensorMap* tmX, const Args& a) {
+  if (lane == 0) {
+    bulk_wait_read<0>();
+    mbar_arrive_expect_tx(auxbar, 2 * kEpiBoxBytes);
+    tma_load_2d(box0, tmX, auxbar, col, row0);
+    tma_load_2d(box1, tmX, auxbar, a.N + col, row0);
+  }
+  __syncwarp();
+  float v[32], du[32];
+  tmem_ld32(taddr, v);
+  const bool got = mbar_wait(auxbar, aux_phase, a.status, kStatusEpilogueTimeout);
+  aux_phase ^= 1u;
+  if (!__all_sync(0xffffffffu, got)) return false;
+  uint4 hp[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint4* p0 = reinterpret_cast<uint4*>(box0 + sw64_off(lane, q));
+    uint4* p1 = reinterpret_cast<uint4*>(box1 + sw64_off(lane, q));
+    float g[8], u[8], h[8];
+    unpack8(*p0, g);
+    unpack8(*p1, u);
+    dglu8(v + 8 * q, g, u, a.act, du + 8 * q, h);
+    *p0 = pack8(v + 8 * q);
+    *p1 = pack8(du + 8 * q);
+    hp[q] = pack8(h);
+  }
+  box_flush(lane, a.out2 != nullptr, [&] {
+    tma_store_2d(tmO, box0, col, row0);
+    tma_store_2d(tmO, box1, a.N + col, row0);
+  });
+  if (a.out2 != nullptr) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)) = hp[q];
+    box_flush(lane, false, [&] { tma_store_2d(tmO2, box0, col, row0); });
+  }
+  epilogue_glu_colsum(v, du, row, col, col_end, lane, a);
+  return true;
+}
+
+// Adds the K slices of 32 columns of a split tile's row, in slice order.
+template <int TM, int TN>
+__device__ __forceinline__ void tail_sum32(const Args& a, const float* base, int cl, int lrow,
+                                           float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 2
+  for (int ks = 0; ks < a.tail_split; ++ks) {
+    const float4* src = reinterpret_cast<const float4*>(base + static_cast<long long>(ks) * TM * TN) +
+                        (cl >> 2) * TM + lrow;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 q = __ldcg(src + i * TM);
+      v[4 * i] += q.x;
+      v[4 * i + 1] += q.y;
+      v[4 * i + 2] += q.z;
+      v[4 * i + 3] += q.w;
+    }
+  }
+}
+
 // The final pass over a split tile, run by the CTA that stored its last
 // slice: each epilogue thread adds its row's 32-column chunks of the
 // tile's slices in slice order (L2 loads: other SMs wrote them) and applies
@@ -632,30 +756,27 @@ __device__ __forceinline__ bool epilogue_chunk_ahead(uint32_t taddr, int lane, i
 template <int TM, int TN, int EPI, int OUT>
 __device__ __forceinline__ void tail_finish(const Args& a, const TileCoord& tc, int ti, int lrow,
                                             int row, int half, int lane) {
+  constexpr int TW = kTileW<TN, EPI>;
   const float* base = a.tail_part + static_cast<long long>(ti) * a.tail_split * TM * TN;
 #pragma unroll 1
-  for (int c = 0; c < TN / 2; c += 32) {
-    const int cl = half * (TN / 2) + c;
+  for (int c = 0; c < TW / 2; c += 32) {
+    const int cl = half * (TW / 2) + c;
     const int col = tc.n0 + cl;
     if (col >= tc.n_end) break;  // warp-uniform
     float v[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
-#pragma unroll 2
-    for (int ks = 0; ks < a.tail_split; ++ks) {
-      const float4* src = reinterpret_cast<const float4*>(base + static_cast<long long>(ks) * TM * TN) +
-                          (cl >> 2) * TM + lrow;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 q = __ldcg(src + i * TM);
-        v[4 * i] += q.x;
-        v[4 * i + 1] += q.y;
-        v[4 * i + 2] += q.z;
-        v[4 * i + 3] += q.w;
-      }
+    tail_sum32<TM, TN>(a, base, cl, lrow, v);
+    if constexpr (EPI == kEpiGlu) {
+      float u[32];
+      tail_sum32<TM, TN>(a, base, TW + cl, lrow, u);
+      epilogue_glu_row32(v, u, row, col, tc.n_end, a);
+    } else if constexpr (EPI == kEpiDGlu) {
+      float du[32];
+      epilogue_dglu_row32(v, du, row, col, tc.n_end, a);
+      epilogue_glu_colsum(v, du, row, col, tc.n_end, lane, a);
+    } else {
+      epilogue_row32<EPI, OUT, false>(v, row, col, tc.n_end, a);
+      epilogue_colsum<EPI>(v, row, col, tc.n_end, lane, a);
     }
-    epilogue_row32<EPI, OUT, false>(v, row, col, tc.n_end, a);
-    epilogue_colsum<EPI>(v, row, col, tc.n_end, lane, a);
   }
 }
 
@@ -743,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; u < args.units && ok; u += gridDim.x) {
         const Unit w = unit_of(u, args);
-        const TileCoord tc = tile_coord<BN>(w.tile, args);
+        const TileCoord tc = tile_coord<kTileW<BN, EPI>>(w.tile, args);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, args.status, kStatusProducerTimeout)) {
             ok = false;
@@ -762,6 +883,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (B_KMAJ) {
             tma_load_2d(b_dst, &tmB, &full[stage], kc, tc.n0);
+          } else if (EPI == kEpiGlu) {
+            // BN / 2 gate columns, then the up columns that belong to them
+#pragma unroll
+            for (int c = 0; c < BN / 64; ++c)
+              tma_load_2d(b_dst + c * (BK * 128), &tmB, &full[stage],
+                          c < BN / 128 ? tc.n0 + 64 * c : args.N + tc.n0 + 64 * (c - BN / 128), kc);
           } else {
 #pragma unroll
             for (int c = 0; c < BN / 64; ++c)
@@ -843,20 +970,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     for (int u = blockIdx.x; u < args.units && ok; u += gridDim.x) {
       const Unit w = unit_of(u, args);
-      const TileCoord tc = tile_coord<BN>(w.tile, args);
-      const uint4 bq = bias_half<EPI, BN / 2>(args, tc.n0 + half * (BN / 2), tc.n_end, lane);
+      constexpr int TW = kTileW<BN, EPI>;
+      const TileCoord tc = tile_coord<TW>(w.tile, args);
+      const uint4 bq = bias_half<EPI, TW / 2>(args, tc.n0 + half * (TW / 2), tc.n_end, lane);
+      uint4 bu = make_uint4(0u, 0u, 0u, 0u);
+      if (EPI == kEpiGlu)
+        bu = bias_half<EPI, TW / 2>(args, args.N + tc.n0 + half * (TW / 2), args.N + tc.n_end, lane);
       if (!mbar_wait(&tfull[acc], acc_phase, args.status, kStatusEpilogueTimeout)) break;
       tc_fence_after();
       const int lrow = quarter * 32 + lane;
       const int row = tc.m0 + lrow;
       const int tg = (EPI == kEpiCE && row < args.M) ? args.ce_target[row] : -1;
 #pragma unroll 1
-      for (int c = 0; c < BN / 2; c += 32) {
-        const int cl = half * (BN / 2) + c;
+      for (int c = 0; c < TW / 2; c += 32) {
+        const int cl = half * (TW / 2) + c;
         const int col = tc.n0 + cl;
         if (col >= tc.n_end) break;  // warp-uniform
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(acc * BN + cl);
+        if constexpr (EPI == kEpiGlu || EPI == kEpiDGlu) {
+          const int row0 = tc.m0 + quarter * 32;
+          if (args.tma_out && w.part < 0 && col + 32 <= tc.n_end) {
+            if constexpr (EPI == kEpiGlu)
+              epilogue_glu_boxed(taddr, taddr + TW, lane, row0, col, box0, box1, &tmO, &tmO2, bq,
+                                 bu, c / 8, args);
+            else
+              ok = epilogue_dglu_boxed(taddr, lane, row, row0, col, tc.n_end, box0, box1,
+                                       &auxbar[ew], aux_phase, &tmO, &tmO2, &tmX, args);
+            if (!ok) break;
+            continue;
+          }
+          float v[32], u[32];
+          tmem_ld32(taddr, v);
+          if constexpr (EPI == kEpiGlu) tmem_ld32(taddr + TW, u);
+          if (w.part >= 0) {
+            float* slice = args.tail_part + static_cast<long long>(w.part) * BM * BN;
+            store_partial32<BM>(v, slice, lrow, cl);
+            if constexpr (EPI == kEpiGlu) store_partial32<BM>(u, slice, lrow, TW + cl);
+          } else if constexpr (EPI == kEpiGlu) {
+            epilogue_glu_row32(v, u, row, col, tc.n_end, args);
+          } else {
+            epilogue_dglu_row32(v, u, row, col, tc.n_end, args);
+            epilogue_glu_colsum(v, u, row, col, tc.n_end, lane, args);
+          }
+          continue;
+        }
         if constexpr (OUT != kOutF32) {
           if (args.tma_out && w.part < 0 && col + 32 <= tc.n_end) {
             if constexpr (LY::kAhead) {
@@ -866,7 +1024,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               // Request the next chunk's: the next one of this tile, or the
               // first one of this CTA's next unit.
               ax_u = -1;
-              if (c + 32 < BN / 2) {
+              if (c + 32 < TW / 2) {
                 if (col + 64 <= tc.n_end) {
                   ax_fetch(slot ^ 1, col + 32, tc.m0 + quarter * 32);
                   ax_u = u;
@@ -875,8 +1033,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               } else if (u + static_cast<int>(gridDim.x) < args.units) {
                 const int un = u + static_cast<int>(gridDim.x);
                 const Unit wn = unit_of(un, args);
-                const TileCoord tn = tile_coord<BN>(wn.tile, args);
-                const int coln = tn.n0 + half * (BN / 2);
+                const TileCoord tn = tile_coord<TW>(wn.tile, args);
+                const int coln = tn.n0 + half * (TW / 2);
                 if (wn.part < 0 && coln + 32 <= tn.n_end) {
                   ax_fetch(slot ^ 1, coln, tn.m0 + quarter * 32);
                   ax_u = un;
@@ -1145,7 +1303,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (col >= tc.n_end) break;  // warp-uniform
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(acc * kPairTN + cl);
-        if constexpr (OUT != kOutF32) {
+        if constexpr (EPI == kEpiDGlu) {
+          if (args.tma_out && w.part < 0 && col + 32 <= tc.n_end) {
+            ok = epilogue_dglu_boxed(taddr, lane, row,
+                                     tc.m0 + 128 * static_cast<int>(rank) + quarter * 32, col,
+                                     tc.n_end, box0, box1, &auxbar[ew], aux_phase, &tmO, &tmO2,
+                                     &tmX, args);
+            if (!ok) break;
+            continue;
+          }
+          float v[32], du[32];
+          tmem_ld32(taddr, v);
+          if (w.part >= 0) {
+            store_partial32<kPairTM>(
+                v, args.tail_part + static_cast<long long>(w.part) * kPairTM * kPairTN, lrow, cl);
+          } else {
+            epilogue_dglu_row32(v, du, row, col, tc.n_end, args);
+            epilogue_glu_colsum(v, du, row, col, tc.n_end, lane, args);
+          }
+          continue;
+        } else if constexpr (OUT != kOutF32) {
           if (args.tma_out && w.part < 0 && col + 32 <= tc.n_end) {
             ok = epilogue_chunk_boxed<EPI, OUT>(
                 taddr, lane, row, tc.m0 + 128 * static_cast<int>(rank) + quarter * 32, col,
@@ -1306,6 +1483,12 @@ bool make_epi_maps(const Gemm& g, EpiMaps& e) {
     return false;
   if ((EPI == kEpiResidual || EPI == kEpiDGelu) && !make_box_map(&e.x, g.aux, g.N, g.M, g.ldaux))
     return false;
+  if (EPI == kEpiGlu && g.out2 != nullptr && !make_box_map(&e.o2, g.out2, 2 * g.N, g.M, g.ldo2))
+    return false;
+  if (EPI == kEpiDGlu && (!make_box_map(&e.o, g.out, 2 * g.N, g.M, g.ldo) ||
+                          !make_box_map(&e.x, g.aux, 2 * g.N, g.M, g.ldaux) ||
+                          (g.out2 != nullptr && !make_box_map(&e.o2, g.out2, g.N, g.M, g.ldo2))))
+    return false;
   return true;
 }
 
@@ -1315,6 +1498,7 @@ struct Plan {
 };
 
 Plan plan_for(const Gemm& g, int bn) {
+  if (g.epi == kEpiGlu) bn /= 2;  // kTileW
   Plan p;
   p.bn = bn;
   p.m_tiles = static_cast<int>((g.M + BM - 1) / BM);
@@ -1405,7 +1589,7 @@ double est_tiles(const Gemm& g, long long T, int workers, size_t part_bytes, dou
 // 192-wide tiles against 66 us on 256-wide ones).
 int choose_tile(const Gemm& g) {
   const int ov = tile_override();
-  if (ov != 0) return ov;
+  if (ov != 0) return g.epi == kEpiGlu && ov != 128 ? 256 : ov;
   const double sms = sm_count();
   double best = 1e300;
   int kind = 256;
@@ -1413,6 +1597,7 @@ int choose_tile(const Gemm& g) {
   const bool short_k = (g.K + BK - 1) / BK <= 16;
   const double rate[3] = {1.0, short_k ? 0.96 : 0.85, short_k ? 0.90 : 0.68};
   for (int i = 0; i < 3; ++i) {
+    if (g.epi == kEpiGlu && widths[i] == 192) continue;  // halves of 96 columns: not built
     const Plan p = plan_for(g, widths[i]);
     const double t = est_tiles(g, static_cast<long long>(p.m_tiles) * p.n_tiles,
                                static_cast<int>(sms), size_t(BM) * widths[i] * 4,
@@ -1422,6 +1607,7 @@ int choose_tile(const Gemm& g) {
       kind = widths[i];
     }
   }
+  if (g.epi == kEpiGlu) return kind;  // single-SM kinds only (the faster ones for this layout)
   double pair_rate;
   if (g.a.k_major && !g.b.k_major)
     pair_rate = 0.96;                                 // forward
@@ -1444,7 +1630,7 @@ tp_status launch_impl(const Gemm& g, cudaStream_t stream) {
   const bool ok_a = AK ? make_map(&ta, g.a.ptr, g.K, g.M, g.a.ld, BK, BM)
                        : make_map(&ta, g.a.ptr, g.M, g.K, g.a.ld, 64, BK);
   const bool ok_b = BKM ? make_map(&tb, g.b.ptr, g.K, g.N, g.b.ld, BK, BN)
-                        : make_map(&tb, g.b.ptr, g.N, g.K, g.b.ld, 64, BK);
+                        : make_map(&tb, g.b.ptr, EPI == kEpiGlu ? 2 * g.N : g.N, g.K, g.b.ld, 64, BK);
   if (!ok_a || !ok_b) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed");
 
   Args a = plan_args(g, BN, false);
@@ -1460,8 +1646,9 @@ tp_status launch_impl(const Gemm& g, cudaStream_t stream) {
   a.ce_cps = g.ce.cps;
   a.ce_target = g.ce.target;
   a.ce_tlogit = g.ce.tlogit;
-  a.csum_part = EPI == kEpiDGelu ? g.csum_part : nullptr;
-  a.csum_ld = g.N;
+  a.csum_part = (EPI == kEpiDGelu || EPI == kEpiDGlu) ? g.csum_part : nullptr;
+  a.csum_ld = EPI == kEpiDGlu ? 2 * g.N : g.N;
+  a.act = g.act;
   a.status = wait_ctl();
   if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
   EpiMaps em;
@@ -1487,11 +1674,12 @@ tp_status launch_impl(const Gemm& g, cudaStream_t stream) {
   const int grid = static_cast<int>(tp.units < sm_count() ? tp.units : sm_count());
   a.tail_ctr = static_cast<unsigned long long*>(g.tail_ws);
   a.tail_part = reinterpret_cast<float*>(static_cast<char*>(g.tail_ws) + kTailCtrBytes);
-  const double flops = 2.0 * double(g.M) * double(g.N) * double(g.K);
-  const double bytes = 2.0 * (double(g.M) * g.K + double(g.K) * g.N) +
-                       (OUT == kOutF32 ? 4.0 : 2.0) * double(g.M) * g.N +
-                       (g.out2 ? 2.0 * double(g.M) * g.N : 0.0) +
-                       (g.aux ? 2.0 * double(g.M) * g.N : 0.0) +
+  const double glu = EPI == kEpiGlu ? 2.0 : 1.0;  // two products per output column
+  const double flops = 2.0 * glu * double(g.M) * double(g.N) * double(g.K);
+  const double bytes = 2.0 * (double(g.M) * g.K + glu * double(g.K) * g.N) +
+                       (OUT == kOutF32 ? 4.0 : EPI == kEpiDGlu ? 4.0 : 2.0) * double(g.M) * g.N +
+                       (g.out2 ? 2.0 * glu * double(g.M) * g.N : 0.0) +
+                       (g.aux ? (EPI == kEpiDGlu ? 4.0 : 2.0) * double(g.M) * g.N : 0.0) +
                        (EPI == kEpiCE ? 8.0 * double(g.M) * g.N / 32.0 : 0.0);
   {
     LaunchScope scope(TP_KIND_GEMM_TCGEN05, flops, bytes, stream, 1, BN, g.M, g.N, g.K);
@@ -1521,6 +1709,12 @@ tp_status dispatch(const Gemm& g, cudaStream_t s) {
     if (ak && bk && plain_out) return launch_impl<BN, true, true, kEpiDGelu, kOutBF16>(g, s);
   } else if (g.epi == kEpiCE) {
     if (ak && bk && plain_out) return launch_impl<BN, true, true, kEpiCE, kOutBF16>(g, s);
+  } else if (g.epi == kEpiGlu) {
+    if constexpr (BN != 192) {
+      if (ak && !bk && plain_out) return launch_impl<BN, true, false, kEpiGlu, kOutBF16>(g, s);
+    }
+  } else if (g.epi == kEpiDGlu) {
+    if (ak && bk && plain_out) return launch_impl<BN, true, true, kEpiDGlu, kOutBF16>(g, s);
   } else {
     if (ak && !bk) return by_out<BN, true, false, kEpiStore>(g, s);
     if (ak && bk) return by_out<BN, true, true, kEpiStore>(g, s);
@@ -1554,8 +1748,9 @@ tp_status launch_pair(const Gemm& g, cudaStream_t stream) {
   a.ce_cps = g.ce.cps;
   a.ce_target = g.ce.target;
   a.ce_tlogit = g.ce.tlogit;
-  a.csum_part = EPI == kEpiDGelu ? g.csum_part : nullptr;
-  a.csum_ld = g.N;
+  a.csum_part = (EPI == kEpiDGelu || EPI == kEpiDGlu) ? g.csum_part : nullptr;
+  a.csum_ld = EPI == kEpiDGlu ? 2 * g.N : g.N;
+  a.act = g.act;
   a.status = wait_ctl();
   if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
   EpiMaps em;
@@ -1598,9 +1793,9 @@ tp_status launch_pair(const Gemm& g, cudaStream_t stream) {
   a.tail_part = reinterpret_cast<float*>(static_cast<char*>(g.tail_ws) + kTailCtrBytes);
   const double flops = 2.0 * double(g.M) * double(g.N) * double(g.K);
   const double bytes = 2.0 * (double(g.M) * g.K + double(g.K) * g.N) +
-                       (OUT == kOutF32 ? 4.0 : 2.0) * double(g.M) * g.N +
+                       (OUT == kOutF32 ? 4.0 : EPI == kEpiDGlu ? 4.0 : 2.0) * double(g.M) * g.N +
                        (g.out2 ? 2.0 * double(g.M) * g.N : 0.0) +
-                       (g.aux ? 2.0 * double(g.M) * g.N : 0.0) +
+                       (g.aux ? (EPI == kEpiDGlu ? 4.0 : 2.0) * double(g.M) * g.N : 0.0) +
                        (EPI == kEpiCE ? 8.0 * double(g.M) * g.N / 32.0 : 0.0);
   {
     LaunchScope scope(TP_KIND_GEMM_TCGEN05, flops, bytes, stream, 1, 512, g.M, g.N, g.K);
@@ -1629,6 +1824,8 @@ tp_status dispatch_pair(const Gemm& g, cudaStream_t s) {
     if (ak && bk && plain_out) return launch_pair<true, true, kEpiDGelu, kOutBF16>(g, s);
   } else if (g.epi == kEpiCE) {
     if (ak && bk && plain_out) return launch_pair<true, true, kEpiCE, kOutBF16>(g, s);
+  } else if (g.epi == kEpiDGlu) {
+    if (ak && bk && plain_out) return launch_pair<true, true, kEpiDGlu, kOutBF16>(g, s);
   } else {
     if (ak && !bk) return pair_by_out<true, false, kEpiStore>(g, s);
     if (ak && bk) return pair_by_out<true, true, kEpiStore>(g, s);
@@ -1706,6 +1903,8 @@ tp_status launch_gemm_bf16(const Gemm& g, cudaStream_t stream) {
        gg.ce.tlogit == nullptr || gg.ce.cps != (gg.n_shard + 31) / 32 ||
        gg.ce.ldp != gg.ce.cps * (gg.N / gg.n_shard)))
     return fail(TP_ERR_SHAPE, "gemm: inconsistent cross-entropy partial layout");
+  if ((gg.epi == kEpiGlu || gg.epi == kEpiDGlu) && 2 * gg.N > (1ll << 31) - 256)
+    return fail(TP_ERR_SHAPE, "gemm: dimension too large");
   switch (choose_tile(gg)) {
     case 512: return dispatch_pair(gg, stream);
     case 128: return dispatch<128>(gg, stream);

@@ -53,6 +53,10 @@ enum Epi : int {
   kEpiResidual = 3,  // out = acc (+ bias[col]) + aux[row,col]: a residual addition
   kEpiCE = 4,        // z = bf16(acc); out = z (if out); per 32-column chunk of a
                      // shard: (max z, sum exp(z - max)) to ce_part; the target's z
+  kEpiGlu = 5,       // B is [Wg | Wu]: g, u = the two products (+ bias halves);
+                     // out = act(g) u; out2 = [g | u] (if out2)
+  kEpiDGlu = 6,      // aux = [g | u]: out = [acc u act'(g) | acc act(g)];
+                     // out2 = act(g) u (if out2)
 };
 
 // Cross-entropy outputs of a kEpiCE GEMM (columns are vocabulary entries).
@@ -102,17 +106,33 @@ struct Gemm {
   const void* aux = nullptr;   // auxiliary input (bf16), ldaux
   int64_t ldaux = 0;
   int64_t n_shard = 0;         // columns per shard: column tiles never straddle shards
+  // kEpiGlu / kEpiDGlu: N is the width of the product act(g) u; the matrices
+  // that hold both halves ([Wg | Wu], [g | u] and its gradient) have 2 N
+  // columns, the second half at column N.  act: tp_act.
+  int act = TP_ACT_SILU;
   KOrder korder;
   CEOut ce;                    // kEpiCE only (requires n_shard % 8 == 0)
-  // kEpiDGelu on the tensor-core path: per-32-row column sums of the output
-  // (fp32, before rounding) to csum_part[(row / 32) * N + col], ceil(M / 32)
-  // rows; finish with launch_colsum_finish.  nullptr: none.
+  // kEpiDGelu / kEpiDGlu on the tensor-core path: per-32-row column sums of the output
+  // (fp32, before rounding) to csum_part[(row / 32) * columns + col], ceil(M /
+  // 32) rows; finish with launch_colsum_finish.  nullptr: none.
   float* csum_part = nullptr;
   // Scratch for splitting the last partial wave of tiles along K (optional;
   // gemm_tail_scratch_bytes() is always enough).
   void* tail_ws = nullptr;
   size_t tail_ws_bytes = 0;
 };
+
+// The gated block's forward on a few tokens (M <= kThinMaxM), by kernels that
+// stream the weights: H = act(x wgu + bgu) ([g | u] to gu unless nullptr), z =
+// H wd + bd.
+constexpr int64_t kThinMaxM = 64;
+struct ThinGlu {
+  const void *x = nullptr, *wgu = nullptr, *bgu = nullptr, *wd = nullptr, *bd = nullptr;
+  void *H = nullptr, *gu = nullptr, *z = nullptr;
+  int64_t M = 0, h = 0, f = 0;
+  int act = TP_ACT_SILU;
+};
+tp_status launch_thin_glu(const ThinGlu& g, cudaStream_t stream);
 
 // Scratch that lets a tcgen05 GEMM split its last wave along K.
 size_t gemm_tail_scratch_bytes();

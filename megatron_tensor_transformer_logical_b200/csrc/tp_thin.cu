@@ -1,0 +1,364 @@
+// The gated feed-forward block on a few tokens: the cost is reading the
+// weights once (2 M flops per weight byte, far below the ridge), so both
+// products stream them.
+//   up:   H = act(X Wg + bg) * (X Wu + bu)   (gate and up columns together)
+//   down: Z = H Wd + bd
+// * A block owns 64 columns of H (its gate and its up columns) or 128 of Z and
+//   a slice of K; its 8 warps are 4 K groups x 2 runs of 64 columns.  A warp
+//   streams its own 16 (K) x 64 (columns) weight tiles, with the tokens' 16
+//   values of K beside them, through its own ring of cp.async stages: no block
+//   barrier in the loop, 128 contiguous bytes per weight row.
+// * m16n8k16 products, 16 tokens as the rows (MT of them per warp), the weight
+//   tile transposed on its way out of shared memory.
+// * The K groups are added through shared memory, the K slices of a tile
+//   (a cluster of blocks) through distributed shared memory, in a fixed
+//   order; then bias, activation and product.  Nothing goes through HBM but
+//   the weights, X, H and Z.
+// * The down product is launched with programmatic stream serialisation: its
+//   blocks start as the up product's finish, request their first weight tiles,
+//   and only then wait for H.
+// All blocks run at once (clusters are sized for that): every block then has
+// the same number of bytes in flight, so they share the HBM evenly and end
+// together whatever the number of blocks per SM.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "epi_math.cuh"
+#include "tp_internal.h"
+
+namespace tp {
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kGroups = 4;  // K groups; kWarps / kGroups = 2 column runs
+constexpr int kCols = 64;   // columns of a run
+constexpr int kStepK = 16;
+constexpr int kMaxCluster = 8;
+
+struct ThinArgs {
+  const __nv_bfloat16 *x, *w, *bias;
+  __nv_bfloat16 *out, *gu;  // gu: [M, 2 N] or nullptr (up product)
+  int M, K, N;              // N: columns of H, or of Z
+  long long ldw;
+  int act;
+  int split;    // blocks per tile (the cluster)
+  int pdl;      // wait for the previous kernel before reading x
+};
+
+template <int MT>
+struct Cfg {
+  static constexpr int kStages = MT == 1 ? 5 : MT == 2 ? 4 : 6;
+  static constexpr int kWBytes = kStepK * kCols * 2;         // 2 KB
+  static constexpr int kXBytes = MT * 16 * kStepK * 2;       // 512 bytes per 16 tokens
+  static constexpr int kStageBytes = kWBytes + kXBytes;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kRed = kWarps * 16 * kCols * 4;       // one m-tile of every warp
+  static constexpr int kSum = 2 * MT * 16 * kCols * 4;       // both runs, K groups added
+  static constexpr int kBytes = kRing > kRed + kSum ? kRing : kRed + kSum;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0 source bytes: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  if (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+template <int MT, bool GLU>
+__global__ void __launch_bounds__(kThreads, MT <= 2 ? 2 : 1) thin_product(const ThinArgs a) {
+  using C = Cfg<MT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = a.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / a.split;
+  const int run = warp & 1, kg = warp >> 1;
+  const int col0 = tile * (GLU ? kCols : 2 * kCols) + (GLU ? 0 : run * kCols);  // output column
+  const int ncols = min(kCols, a.N - col0);  // may be <= 0: the run is past the edge
+  const __nv_bfloat16* w = a.w + col0 + (GLU ? run * static_cast<long long>(a.N) : 0);
+
+  const int steps = (a.K + kStepK - 1) / kStepK;
+  const int s0 = static_cast<int>(static_cast<long long>(steps) * rank / a.split) + kg;
+  const int s1 = static_cast<int>(static_cast<long long>(steps) * (rank + 1) / a.split);
+  const int n = s0 < s1 ? (s1 - s0 + kGroups - 1) / kGroups : 0;
+
+  const uint32_t ring = smem_u32(smem) + warp * C::kStages * C::kStageBytes;
+  // Weight rows k .. k + 15 of this warp's i-th step: 16-byte chunk j of row r
+  // at chunk j ^ (r & 7).
+  auto fetch_w = [&](int i) {
+    const uint32_t st = ring + (i % C::kStages) * C::kStageBytes;
+    const int k = (s0 + i * kGroups) * kStepK;
+    const int j = lane & 7;
+    const bool okc = 8 * j + 8 <= ncols;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = x * 4 + (lane >> 3);
+      const bool ok = okc && k + r < a.K;
+      cp_async16(st + r * 128 + ((j ^ (r & 7)) << 4),
+                 ok ? w + static_cast<long long>(k + r) * a.ldw + 8 * j : a.w, ok);
+    }
+  };
+  // The tokens' values of the same K: 16-byte half h of token t (32-byte rows)
+  // at half h ^ bit 2 of t.
+  auto fetch_x = [&](int i) {
+    const uint32_t st = ring + (i % C::kStages) * C::kStageBytes + C::kWBytes;
+    const int k = (s0 + i * kGroups) * kStepK + 8 * (lane & 1);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int t = 16 * mt + (lane >> 1);
+      const bool ok = t < a.M && k < a.K;
+      cp_async16(st + t * 32 + (((lane & 1) ^ ((t >> 2) & 1)) << 4),
+                 ok ? a.x + static_cast<long long>(t) * a.K + k : a.x, ok);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i)
+    if (i < n) fetch_w(i);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < C::kStages - 1; ++i) {
+    if (i < n) fetch_x(i);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  float acc[MT][kCols / 8][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int c = 0; c < kCols / 8; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[mt][c][e] = 0.0f;
+
+  const int wrow = (lane & 7) + (((lane >> 3) & 1) << 3), wcol = lane >> 4;
+  const int xrow = lane & 15, xhalf = lane >> 4;
+  for (int i = 0; i < n; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+    __syncwarp();  // all lanes' copies of this stage have landed; the stage
+                   // fetched below has been read by every lane
+    if (i + C::kStages - 1 < n) {
+      fetch_w(i + C::kStages - 1);
+      fetch_x(i + C::kStages - 1);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t sw = ring + (i % C::kStages) * C::kStageBytes, sx = sw + C::kWBytes;
+    uint32_t xf[MT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int t = 16 * mt + xrow;
+      ldmatrix4<false>(xf[mt], sx + t * 32 + ((xhalf ^ ((t >> 2) & 1)) << 4));
+    }
+#pragma unroll
+    for (int c = 0; c < kCols / 16; ++c) {
+      uint32_t b[4];
+      ldmatrix4<true>(b, sw + wrow * 128 + (((2 * c + wcol) ^ (wrow & 7)) << 4));
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma16816(acc[mt][2 * c], xf[mt], b[0], b[1]);
+        mma16816(acc[mt][2 * c + 1], xf[mt], b[2], b[3]);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+  // Add the K groups, 16 tokens at a time.
+  float* red = reinterpret_cast<float*>(smem);                    // [warp][16][kCols]
+  float* sum = reinterpret_cast<float*>(smem + C::kRed);          // [run][16 MT][kCols]
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();  // the rings / the previous tokens' values are done with
+#pragma unroll
+    for (int c = 0; c < kCols / 8; ++c) {
+      float* d = red + (warp * 16 + (lane >> 2)) * kCols + 8 * c + 2 * (lane & 3);
+      *reinterpret_cast<float2*>(d) = make_float2(acc[mt][c][0], acc[mt][c][1]);
+      *reinterpret_cast<float2*>(d + 8 * kCols) = make_float2(acc[mt][c][2], acc[mt][c][3]);
+    }
+    __syncthreads();
+    for (int x = threadIdx.x; x < 2 * 16 * kCols / 2; x += kThreads) {
+      const int rn = x / (16 * kCols / 2), y = x - rn * (16 * kCols / 2);
+      float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q) {
+        const float2 v = reinterpret_cast<const float2*>(red + (2 * q + rn) * 16 * kCols)[y];
+        s.x += v.x;
+        s.y += v.y;
+      }
+      reinterpret_cast<float2*>(sum + (rn * MT + mt) * 16 * kCols)[y] = s;
+    }
+  }
+  if (a.split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+
+  // The tile's slices, in rank order; each block finishes its share of the
+  // column pairs.
+  const uint32_t base = smem_u32(sum);
+  auto total = [&](int rn, int t, int c) {
+    const uint32_t off = base + static_cast<uint32_t>(((rn * MT * 16 + t) * kCols + c) * 4);
+    float2 s = make_float2(0.0f, 0.0f);
+    for (int r = 0; r < a.split; ++r) {
+      const float2 v = a.split > 1 ? ld_cluster2(mapa_shared(off, r))
+                                   : *reinterpret_cast<const float2*>(
+                                         sum + (rn * MT * 16 + t) * kCols + c);
+      s.x += v.x;
+      s.y += v.y;
+    }
+    return s;
+  };
+  auto bias2 = [&](int col) {
+    if (a.bias == nullptr) return make_float2(0.0f, 0.0f);
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(a.bias + col));
+  };
+  const int pairs = (GLU ? kCols : 2 * kCols) / 2;
+  const int tcol = tile * 2 * pairs;  // first output column of the tile
+  for (int x = rank * kThreads + threadIdx.x; x < a.M * pairs; x += a.split * kThreads) {
+    const int t = x / pairs, c = 2 * (x - t * pairs);
+    const int col = tcol + c;
+    if (col >= a.N) continue;
+    if (GLU) {
+      float2 g = total(0, t, c), u = total(1, t, c);
+      const float2 bg = bias2(col), bu = bias2(a.N + col);
+      g.x += bg.x;
+      g.y += bg.y;
+      u.x += bu.x;
+      u.y += bu.y;
+      if (a.gu != nullptr) {
+        __nv_bfloat16* p = a.gu + static_cast<long long>(t) * 2 * a.N + col;
+        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(g.x, g.y);
+        *reinterpret_cast<__nv_bfloat162*>(p + a.N) = __floats2bfloat162_rn(u.x, u.y);
+      }
+      const float2 v = gate_act2(g, a.act);
+      *reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<long long>(t) * a.N + col) =
+          __floats2bfloat162_rn(v.x * u.x, v.y * u.y);
+    } else {
+      float2 z = total(c / kCols, t, c % kCols);
+      const float2 b = bias2(col);
+      *reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<long long>(t) * a.N + col) =
+          __floats2bfloat162_rn(z.x + b.x, z.y + b.y);
+    }
+  }
+  if (a.split > 1) {
+    __syncwarp();
+    cluster_sync();  // no block leaves while its sums are read
+  }
+}
+
+// Blocks per tile: the largest cluster with which all blocks still run at
+// once (two per SM, one with 4 m-tiles) and every warp keeps a few steps.
+int plan_split(int tiles, int K, int per_sm) {
+  const int steps = (K + kStepK - 1) / kStepK;
+  int s = 1;
+  while (2 * s <= kMaxCluster && tiles * 2LL * s <= static_cast<long long>(per_sm) * sm_count() &&
+         steps >= 2 * s * kGroups * 4)
+    s *= 2;
+  return s;
+}
+
+template <int MT, bool GLU>
+tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
+  constexpr int smem = Cfg<MT>::kBytes;
+  auto kern = thin_product<MT, GLU>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "thin product smem");
+  const int width = GLU ? kCols : 2 * kCols;
+  const int tiles = (a.N + width - 1) / width;
+  a.split = plan_split(tiles, a.K, MT <= 2 ? 2 : 1);
+  a.pdl = pdl ? 1 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * a.split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int na = 0;
+  if (a.split > 1) {
+    attr[na].id = cudaLaunchAttributeClusterDimension;
+    attr[na].val.clusterDim.x = a.split;
+    attr[na].val.clusterDim.y = 1;
+    attr[na].val.clusterDim.z = 1;
+    ++na;
+  }
+  if (pdl) {
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = na;
+  const double cols = (GLU ? 2.0 : 1.0) * a.N;
+  LaunchScope scope(TP_KIND_GEMM_TCGEN05, 2.0 * a.M * a.K * cols,
+                    2.0 * (a.K * cols + double(a.M) * a.K + double(a.M) * a.N), stream, 1, 16 * MT,
+                    a.M, a.N, a.K);
+  e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? TP_OK : cuda_fail(e, "thin product launch");
+}
+
+template <bool GLU>
+tp_status launch_m(const ThinArgs& a, bool pdl, cudaStream_t stream) {
+  if (a.M <= 16) return launch<1, GLU>(a, pdl, stream);
+  if (a.M <= 32) return launch<2, GLU>(a, pdl, stream);
+  return launch<4, GLU>(a, pdl, stream);
+}
+
+}  // namespace
+
+tp_status launch_thin_glu(const ThinGlu& g, cudaStream_t stream) {
+  ThinArgs a{};
+  a.M = static_cast<int>(g.M);
+  a.act = g.act;
+  a.x = static_cast<const __nv_bfloat16*>(g.x);
+  a.w = static_cast<const __nv_bfloat16*>(g.wgu);
+  a.bias = static_cast<const __nv_bfloat16*>(g.bgu);
+  a.out = static_cast<__nv_bfloat16*>(g.H);
+  a.gu = static_cast<__nv_bfloat16*>(g.gu);
+  a.K = static_cast<int>(g.h);
+  a.N = static_cast<int>(g.f);
+  a.ldw = 2 * g.f;
+  tp_status s = launch_m<true>(a, false, stream);
+  if (s != TP_OK) return s;
+  a.x = static_cast<const __nv_bfloat16*>(g.H);
+  a.w = static_cast<const __nv_bfloat16*>(g.wd);
+  a.bias = static_cast<const __nv_bfloat16*>(g.bd);
+  a.out = static_cast<__nv_bfloat16*>(g.z);
+  a.gu = nullptr;
+  a.K = static_cast<int>(g.f);
+  a.N = static_cast<int>(g.h);
+  a.ldw = g.h;
+  return launch_m<false>(a, true, stream);
+}
+
+}  // namespace tp
