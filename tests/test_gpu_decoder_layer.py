@@ -6,8 +6,12 @@ rotary positions, windowed attention, output projection, gated block.
 
 Tolerances: normwise, from the bf16 roundings in a row (1.7e-3 each, see
 parity.py's 5e-3 for up to eight of them added in squares).  X2 passes through
-eight (QKV, Q/K, P, O, the projection, X1, H, Z); a gradient through about
-twice as many: sqrt(20) * 1.7e-3 = 7.6e-3.
+eight (QKV, Q/K, P, O, the projection, X1, H, Z).  The longest gradient, gq's,
+meets twenty: QKV as q, k and v, Qr, Kr, P, O, the projection, X1, G, U, [dG |
+dU], dX1 twice, dO, P and dS, dQr, dQ and its own: sqrt(20) * 1.7e-3 = 7.6e-3.
+That is the root mean square; the norm of n independent errors scatters about
+it by a relative 1 / sqrt(2 n), and the norm weights have only n = 64 values,
+so four such deviations are allowed: 7.6e-3 * (1 + 4 / sqrt(2 n)).
 """
 import pytest
 import torch
@@ -123,7 +127,7 @@ def test_training_step():
     assert normwise(X2, ref.detach()) <= 5e-3
     for n in rg:
         nw = normwise(grads[n], rg[n])
-        assert nw <= 7.6e-3, (n, nw)
+        assert nw <= 7.6e-3 * (1 + 4 / (2 * rg[n].numel()) ** 0.5), (n, nw)
 
 
 def test_generation_follows_the_prompt():
