@@ -412,7 +412,7 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  *   X [M, h]; bgu [2f] = [bg | bu] or NULL; Wd [f, h]; bd [h] or NULL;
  *   Z [M, h]; GUsave [M, 2f] = [G | U] (rounded to bf16) or NULL: kept for
  *   the backward.  H is rounded to bf16 and lives in the workspace.
- *   Up to 64 tokens take kernels that stream the weights once (a token's
+ *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
  *   larger batches'.
  * Errors: NULL X / Wgu / Wd / Z; f % t; alignment (h, f multiples of 8);

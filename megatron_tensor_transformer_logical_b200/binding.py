@@ -323,66 +323,85 @@ def tp_vocab_ce_bwd(X, E, targets, logits, lse, dloss, dlogits, dX, dE, t: int,
                                   _dtype(X), _stream(stream)))
 
 
+# The calls below are short enough for their Python to show (a decoding step),
+# so each tensor's checks are few attribute reads and the stream is read raw.
 _DTYPES = {torch.float32: TP_F32, torch.bfloat16: TP_BF16, torch.float16: TP_F16}
+_HALF = {torch.bfloat16: TP_BF16, torch.float16: TP_F16}
 
 
-def _rows(t: Optional[torch.Tensor], like: torch.Tensor, what: str):
-    """(pointer, row stride) of a 2-D tensor whose rows are dense."""
-    if t is None:
-        return None, 0
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a 2-D tensor with dense rows is required")
-    if t.dtype != like.dtype or t.device != like.device:
-        raise ValueError(f"{what}: dtype or device differs from the first tensor's")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _bad(t, what: str, shape, dtype, dev: int):
+    raise ValueError(f"{what}: {tuple(shape)} of {dtype} with dense rows on cuda:{dev} is required"
+                     f", not {tuple(t.shape)} of {t.dtype} on {t.device}")
 
 
-def _side(t: Optional[torch.Tensor], n: int, dtype, like: torch.Tensor, what: str):
-    """Pointer of a dense 1-D side tensor of n elements (or None)."""
+def _rows(t, what: str, shape, dtype, dev: int):
+    """(pointer, row stride) of a 2-D tensor of this shape whose rows are dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _bad(t, what, shape, dtype, dev)
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] > 1:
+        _bad(t, what, shape, dtype, dev)
+    return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+
+
+def _flat(t, what: str, n: int, dtype, dev: int):
+    """Pointer of a dense tensor of n elements (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or t.device != like.device:
-        raise ValueError(f"{what}: {n} elements of {dtype} on {like.device} are required")
-    return _ptr(t)
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, what, (n,), dtype, dev)
+    return t.data_ptr()
 
 
-class _on:
-    """Makes the tensors' device current for the call and yields its stream
-    (the given one, else the device's current stream)."""
-
-    def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            raise ValueError("libtp takes CUDA tensors")
-        self.dev, self.stream, self.prev = t.device.index, stream, -1
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        if cur != self.dev:
-            self.prev = cur
-            torch.cuda.set_device(self.dev)
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        if self.prev >= 0:
-            torch.cuda.set_device(self.prev)
+def _ws(ws, dev: int):
+    """(pointer, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a dense tensor on cuda:{dev} is required")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _same_shape(t: Optional[torch.Tensor], like: Optional[torch.Tensor], what: str) -> None:
-    if t is not None and (like is None or t.shape != like.shape):
-        raise ValueError(f"{what}: wrong shape {tuple(t.shape)}")
+def _device_of(t) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libtp takes CUDA tensors")
+    return dev
 
 
-def _qk_sizes(Q, K, gq, gk, pos, inv_freq, d: int):
-    M, nq = Q.shape
-    nk = 0 if K is None else K.shape[1]
-    if Q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {Q.dtype}")
-    if d <= 0 or nq % d or nk % d or (K is not None and K.shape[0] != M):
+def _elsewhere(dev: int, fn, *args) -> bool:
+    """Calls fn(*args) with device `dev` current, if it is not already."""
+    if torch._C._cuda_getDevice() == dev:
+        return False
+    with torch.cuda.device(dev):
+        fn(*args)
+    return True
+
+
+def _raw_stream(stream, dev: int):
+    """The given stream's handle, else that of the device's current stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return getattr(stream, "cuda_stream", stream)
+
+
+def _qk_sizes(Q, K, gq, gk, pos, inv_freq, d: int, dev: int):
+    sq = Q.shape
+    M, nq = sq
+    dt = Q.dtype
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported dtype {dt}")
+    sk = None if K is None else K.shape
+    nk = 0 if K is None else sk[1]
+    if d <= 0 or nq % d or nk % d or (K is not None and sk[0] != M):
         raise ValueError("Q [M, heads * d] and K [M, kv_heads * d] are required")
-    d_rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return (M, nq // d, nk // d, d_rot, _side(gq, d, Q.dtype, Q, "gq"),
-            _side(gk, d, Q.dtype, Q, "gk"), _side(pos, M, torch.int32, Q, "pos"),
-            _side(inv_freq, d_rot // 2, torch.float64, Q, "inv_freq"))
+    nf = 0 if inv_freq is None else inv_freq.numel()
+    return (sq, sk, dt, M, nq // d, nk // d, 2 * nf, _flat(gq, "gq", d, dt, dev),
+            _flat(gk, "gk", d, dt, dev), _flat(pos, "pos", M, torch.int32, dev),
+            _flat(inv_freq, "inv_freq", nf, torch.float64, dev))
+
+
+_NONE = (None, 0)
 
 
 def tp_qk_norm_rope_fwd(Q, K, gq, gk, pos, inv_freq, Qo, Ko, d: int, norm: bool = True,
@@ -390,15 +409,21 @@ def tp_qk_norm_rope_fwd(Q, K, gq, gk, pos, inv_freq, Qo, Ko, d: int, norm: bool 
     """Qo, Ko = rotary(RMSNorm(Q, K)) per head of d columns; Q [M, heads * d], K
     [M, kv_heads * d] (row-strided views allowed, K may be None), pos int32 [M],
     inv_freq fp64 [d_rot / 2] (None: no rotation).  Qo may be Q, Ko may be K."""
-    M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq, d)
-    _same_shape(Qo, Q, "Qo")
-    _same_shape(Ko, K, "Ko")
-    (q, ldq), (k, ldk) = _rows(Q, Q, "Q"), _rows(K, Q, "K")
-    (qo, ldqo), (ko, ldko) = _rows(Qo, Q, "Qo"), _rows(Ko, Q, "Ko")
-    with _on(Q, stream) as st:
-        _check(load().tp_qk_norm_rope_fwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, qo, ldqo, ko, ldko,
-                                          M, heads, kv, d, d_rot, int(norm), int(interleaved), eps,
-                                          _DTYPES[Q.dtype], st))
+    dev = _device_of(Q)
+    if _elsewhere(dev, tp_qk_norm_rope_fwd, Q, K, gq, gk, pos, inv_freq, Qo, Ko, d, norm,
+                  interleaved, eps, stream):
+        return
+    sq, sk, dt, M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq,
+                                                                     d, dev)
+    q, ldq = _rows(Q, "Q", sq, dt, dev)
+    qo, ldqo = _rows(Qo, "Qo", sq, dt, dev)
+    k, ldk = _NONE if K is None else _rows(K, "K", sk, dt, dev)
+    ko, ldko = _NONE if K is None else _rows(Ko, "Ko", sk, dt, dev)
+    status = load().tp_qk_norm_rope_fwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, qo, ldqo, ko, ldko, M,
+                                        heads, kv, d, d_rot, norm, interleaved, eps, _DTYPES[dt],
+                                        _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk, d: int, ws,
@@ -406,21 +431,26 @@ def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk,
                         stream=None) -> None:
     """Backward of tp_qk_norm_rope_fwd from its inputs Q, K and the gradients dQo,
     dKo of its outputs; dQ may be dQo, dK may be dKo; dgq, dgk may be None."""
-    M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq, d)
-    for t, n in ((dQo, "dQo"), (dQ, "dQ")):
-        _same_shape(t, Q, n)
-    for t, n in ((dKo, "dKo"), (dK, "dK")):
-        _same_shape(t, K, n)
-    (q, ldq), (k, ldk) = _rows(Q, Q, "Q"), _rows(K, Q, "K")
-    (gqo, lgqo), (gko, lgko) = _rows(dQo, Q, "dQo"), _rows(dKo, Q, "dKo")
-    (dq, lddq), (dk, lddk) = _rows(dQ, Q, "dQ"), _rows(dK, Q, "dK")
-    with _on(Q, stream) as st:
-        _check(load().tp_qk_norm_rope_bwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, gqo, lgqo, gko, lgko,
-                                          dq, lddq, dk, lddk, _side(dgq, d, Q.dtype, Q, "dgq"),
-                                          _side(dgk, d, Q.dtype, Q, "dgk"), M, heads, kv, d, d_rot,
-                                          int(norm), int(interleaved), eps, _DTYPES[Q.dtype],
-                                          _ptr(ws), 0 if ws is None else ws.numel() *
-                                          ws.element_size(), st))
+    dev = _device_of(Q)
+    if _elsewhere(dev, tp_qk_norm_rope_bwd, Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq,
+                  dgk, d, ws, norm, interleaved, eps, stream):
+        return
+    sq, sk, dt, M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq,
+                                                                     d, dev)
+    q, ldq = _rows(Q, "Q", sq, dt, dev)
+    gqo, lgqo = _rows(dQo, "dQo", sq, dt, dev)
+    dq, lddq = _rows(dQ, "dQ", sq, dt, dev)
+    k, ldk = _NONE if K is None else _rows(K, "K", sk, dt, dev)
+    gko, lgko = _NONE if K is None else _rows(dKo, "dKo", sk, dt, dev)
+    dk, lddk = _NONE if K is None else _rows(dK, "dK", sk, dt, dev)
+    w, wb = _ws(ws, dev)
+    status = load().tp_qk_norm_rope_bwd(q, ldq, k, ldk, pgq, pgk, ppos, pfr, gqo, lgqo, gko, lgko,
+                                        dq, lddq, dk, lddk, _flat(dgq, "dgq", d, dt, dev),
+                                        _flat(dgk, "dgk", d, dt, dev), M, heads, kv, d, d_rot,
+                                        norm, interleaved, eps, _DTYPES[dt], w, wb,
+                                        _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def qk_norm_rope_workspace(M: int, d: int, device="cuda") -> torch.Tensor:
@@ -428,57 +458,61 @@ def qk_norm_rope_workspace(M: int, d: int, device="cuda") -> torch.Tensor:
     return workspace(TP_OP_QK_NORM_ROPE_BWD, M, d, 0, 0, 1, TP_BF16, device)
 
 
-def _glu_sizes(X, Wgu, Wd, tensors):
+def _glu_sizes(X, Wgu, Wd):
+    """(device, dtype, M, h, f) and the pointers of the inputs."""
+    dev, dt = _device_of(X), X.dtype
     M, h = X.shape
     f = Wd.shape[0]
     if Wgu.shape != (h, 2 * f) or Wd.shape[1] != h:
         raise ValueError("X [M, h], Wgu [h, 2 f] and Wd [f, h] are required")
-    for t, shape, n in ((Wgu, (h, 2 * f), "Wgu"), (Wd, (f, h), "Wd")) + tensors(M, h, f):
-        if t is not None and (t.numel() != torch.Size(shape).numel() or t.dtype != X.dtype
-                              or t.device != X.device):
-            raise ValueError(f"{n}: {shape} of {X.dtype} on {X.device} is required")
-    return M, h, f
+    return (dev, dt, M, h, f, _flat(X, "X", M * h, dt, dev),
+            _flat(Wgu, "Wgu", 2 * h * f, dt, dev), _flat(Wd, "Wd", h * f, dt, dev))
 
 
 def tp_glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, t: int, act: int, ws, stream=None) -> None:
     """Z = (act(X Wg + bg) * (X Wu + bu)) Wd + bd with Wgu = [Wg | Wu] [h, 2 f];
     GUsave [M, 2 f] (or None) keeps [G | U] for the backward."""
-    M, h, f = _glu_sizes(X, Wgu, Wd, lambda M, h, f: (
-        (bgu, (2 * f,), "bgu"), (bd, (h,), "bd"), (Z, (M, h), "Z"), (GUsave, (M, 2 * f), "GUsave")))
-    with _on(X, stream) as st:
-        _check(load().tp_glu_fwd(_ptr(X), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(bd), _ptr(Z),
-                                 _ptr(GUsave), M, h, f, t, act, _dtype(X), _ptr(ws),
-                                 ws.numel() * ws.element_size(), st))
+    dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
+    if _elsewhere(dev, tp_glu_fwd, X, Wgu, bgu, Wd, bd, Z, GUsave, t, act, ws, stream):
+        return
+    w, wb = _ws(ws, dev)
+    status = load().tp_glu_fwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
+                               _flat(bd, "bd", h, dt, dev), _flat(Z, "Z", M * h, dt, dev),
+                               _flat(GUsave, "GUsave", 2 * M * f, dt, dev), M, h, f, t, act,
+                               _dtype(X), w, wb, _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def tp_glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t: int, act: int, ws,
                stream=None) -> None:
     """Backward of tp_glu_fwd; GUsave None recomputes [G | U]; dbgu, dbd may be None."""
-    M, h, f = _glu_sizes(X, Wgu, Wd, lambda M, h, f: (
-        (bgu, (2 * f,), "bgu"), (GUsave, (M, 2 * f), "GUsave"), (dZ, (M, h), "dZ"),
-        (dX, (M, h), "dX"), (dWgu, (h, 2 * f), "dWgu"), (dbgu, (2 * f,), "dbgu"),
-        (dWd, (f, h), "dWd"), (dbd, (h,), "dbd")))
-    with _on(X, stream) as st:
-        _check(load().tp_glu_bwd(_ptr(X), _ptr(Wgu), _ptr(bgu), _ptr(Wd), _ptr(GUsave), _ptr(dZ),
-                                 _ptr(dX), _ptr(dWgu), _ptr(dbgu), _ptr(dWd), _ptr(dbd), M, h, f, t,
-                                 act, _dtype(X), _ptr(ws), ws.numel() * ws.element_size(), st))
+    dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
+    if _elsewhere(dev, tp_glu_bwd, X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t, act,
+                  ws, stream):
+        return
+    w, wb = _ws(ws, dev)
+    status = load().tp_glu_bwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
+                               _flat(GUsave, "GUsave", 2 * M * f, dt, dev),
+                               _flat(dZ, "dZ", M * h, dt, dev), _flat(dX, "dX", M * h, dt, dev),
+                               _flat(dWgu, "dWgu", 2 * h * f, dt, dev),
+                               _flat(dbgu, "dbgu", 2 * f, dt, dev),
+                               _flat(dWd, "dWd", h * f, dt, dev), _flat(dbd, "dbd", h, dt, dev), M,
+                               h, f, t, act, _dtype(X), w, wb, _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
-def _heads(x, n: int, what: str) -> int:
-    """Head dimension of [.., n * d] columns."""
-    if n <= 0 or x.shape[-1] % n:
-        raise ValueError(f"{what}: {x.shape[-1]} columns do not hold {n} heads")
-    return x.shape[-1] // n
-
-
-def _window_sizes(Q, K, V, b: int, heads: int, kv_heads: int):
-    if Q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {Q.dtype}")
-    d = _heads(Q, heads, "Q")
-    if b <= 0 or Q.shape[0] % b or K.shape[0] % b or K.shape[1] != kv_heads * d:
+def _window_sizes(Q, K, b: int, heads: int, kv_heads: int):
+    sq, sk, dt = Q.shape, K.shape, Q.dtype
+    if dt not in _HALF:
+        raise ValueError(f"unsupported dtype {dt}")
+    if heads <= 0 or sq[1] % heads:
+        raise ValueError(f"Q: {sq[1]} columns do not hold {heads} heads")
+    d = sq[1] // heads
+    if b <= 0 or sq[0] % b or sk[0] % b or sk[1] != kv_heads * d:
         raise ValueError("Q [b * sq, heads * d] and K [b * sk, kv_heads * d] are required")
-    _same_shape(V, K, "V")
-    return Q.shape[0] // b, K.shape[0] // b, d
+    return sq, sk, dt, sq[0] // b, sk[0] // b, d
 
 
 def tp_window_attn_fwd(Q, K, V, O, LSE, b: int, heads: int, kv_heads: int, window: int,
@@ -487,34 +521,42 @@ def tp_window_attn_fwd(Q, K, V, O, LSE, b: int, heads: int, kv_heads: int, windo
     d] (row-strided views allowed): each query sees itself, the window - 1 keys
     before it and the first `sinks` keys.  LSE fp32 [b, heads, sq]; scale 0: 1 /
     sqrt(d)."""
-    sq, sk, d = _window_sizes(Q, K, V, b, heads, kv_heads)
-    _same_shape(O, Q, "O")
-    (q, ldq), (k, ldk), (v, ldv), (o, ldo) = (_rows(Q, Q, "Q"), _rows(K, Q, "K"),
-                                              _rows(V, Q, "V"), _rows(O, Q, "O"))
-    lse = _side(LSE, b * heads * sq, torch.float32, Q, "LSE")
-    with _on(Q, stream) as st:
-        _check(load().tp_window_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, b, sq, sk, heads,
-                                         kv_heads, d, window, sinks, scale, _DTYPES[Q.dtype], st))
+    dev = _device_of(Q)
+    if _elsewhere(dev, tp_window_attn_fwd, Q, K, V, O, LSE, b, heads, kv_heads, window, sinks,
+                  scale, stream):
+        return
+    shq, shk, dt, sq, sk, d = _window_sizes(Q, K, b, heads, kv_heads)
+    q, ldq = _rows(Q, "Q", shq, dt, dev)
+    k, ldk = _rows(K, "K", shk, dt, dev)
+    v, ldv = _rows(V, "V", shk, dt, dev)
+    o, ldo = _rows(O, "O", shq, dt, dev)
+    status = load().tp_window_attn_fwd(q, ldq, k, ldk, v, ldv, o, ldo,
+                                       _flat(LSE, "LSE", b * heads * sq, torch.float32, dev), b, sq,
+                                       sk, heads, kv_heads, d, window, sinks, scale, _HALF[dt],
+                                       _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def tp_window_attn_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, b: int, heads: int, kv_heads: int,
                        window: int, sinks: int, ws, scale: float = 0.0, stream=None) -> None:
     """Backward of tp_window_attn_fwd; ws from window_attn_workspace()."""
-    sq, sk, d = _window_sizes(Q, K, V, b, heads, kv_heads)
-    for t, n in ((O, "O"), (dO, "dO"), (dQ, "dQ")):
-        _same_shape(t, Q, n)
-    for t, n in ((dK, "dK"), (dV, "dV")):
-        _same_shape(t, K, n)
-    (q, ldq), (k, ldk), (v, ldv), (o, ldo) = (_rows(Q, Q, "Q"), _rows(K, Q, "K"),
-                                              _rows(V, Q, "V"), _rows(O, Q, "O"))
-    (go, lgo), (gq, lgq), (gk, lgk), (gv, lgv) = (_rows(dO, Q, "dO"), _rows(dQ, Q, "dQ"),
-                                                  _rows(dK, Q, "dK"), _rows(dV, Q, "dV"))
-    lse = _side(LSE, b * heads * sq, torch.float32, Q, "LSE")
-    with _on(Q, stream) as st:
-        _check(load().tp_window_attn_bwd(q, ldq, k, ldk, v, ldv, o, ldo, lse, go, lgo, gq, lgq, gk,
-                                         lgk, gv, lgv, b, sq, sk, heads, kv_heads, d, window,
-                                         sinks, scale, _DTYPES[Q.dtype], _ptr(ws),
-                                         ws.numel() * ws.element_size(), st))
+    dev = _device_of(Q)
+    if _elsewhere(dev, tp_window_attn_bwd, Q, K, V, O, LSE, dO, dQ, dK, dV, b, heads, kv_heads,
+                  window, sinks, ws, scale, stream):
+        return
+    shq, shk, dt, sq, sk, d = _window_sizes(Q, K, b, heads, kv_heads)
+    args = []
+    for t, n, sh in ((Q, "Q", shq), (K, "K", shk), (V, "V", shk), (O, "O", shq)):
+        args += _rows(t, n, sh, dt, dev)
+    args.append(_flat(LSE, "LSE", b * heads * sq, torch.float32, dev))
+    for t, n, sh in ((dO, "dO", shq), (dQ, "dQ", shq), (dK, "dK", shk), (dV, "dV", shk)):
+        args += _rows(t, n, sh, dt, dev)
+    w, wb = _ws(ws, dev)
+    status = load().tp_window_attn_bwd(*args, b, sq, sk, heads, kv_heads, d, window, sinks, scale,
+                                       _HALF[dt], w, wb, _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def tp_window_attn_decode(Q, K, V, lens, O, LSE, heads: int, kv_heads: int, window: int,
@@ -522,28 +564,35 @@ def tp_window_attn_decode(Q, K, V, lens, O, LSE, heads: int, kv_heads: int, wind
     """One token per sequence over a cache: Q, O [b, heads * d], K, V [b, cap,
     kv_heads * d] (strided views allowed), lens int32 [b] on the device (keys per
     sequence, the new token's included), LSE fp32 [b, heads] or None."""
-    if Q.dtype not in _DTYPES:
-        raise ValueError(f"unsupported dtype {Q.dtype}")
-    b, d = Q.shape[0], _heads(Q, heads, "Q")
-    if K.dim() != 3 or K.shape[0] != b or K.shape[2] != kv_heads * d or K.stride(2) != 1 \
-            or V.stride(2) != 1:
-        raise ValueError("K, V [b, cap, kv_heads * d] with dense rows are required")
-    _same_shape(O, Q, "O")
-    _same_shape(V, K, "V")
+    dev = _device_of(Q)
+    if _elsewhere(dev, tp_window_attn_decode, Q, K, V, lens, O, LSE, heads, kv_heads, window,
+                  sinks, ws, scale, stream):
+        return
+    shq, shk, dt = Q.shape, K.shape, Q.dtype
+    if dt not in _HALF:
+        raise ValueError(f"unsupported dtype {dt}")
+    b, nq = shq
+    if heads <= 0 or nq % heads:
+        raise ValueError(f"Q: {nq} columns do not hold {heads} heads")
+    d = nq // heads
+    if len(shk) != 3 or shk[0] != b or shk[2] != kv_heads * d:
+        raise ValueError("K, V [b, cap, kv_heads * d] are required")
+    cap = shk[1]
+    cache = []
     for t, n in ((K, "K"), (V, "V")):
-        if t.dtype != Q.dtype or t.device != Q.device:
-            raise ValueError(f"{n}: dtype or device differs from the first tensor's")
-    cap = K.shape[1]
-    (q, ldq), (o, ldo) = _rows(Q, Q, "Q"), _rows(O, Q, "O")
-    ldk, ldv = (t.stride(1) if cap > 1 else t.shape[2] for t in (K, V))
-    bsk, bsv = (t.stride(0) if b > 1 else 0 for t in (K, V))
-    plens = _side(lens, b, torch.int32, Q, "lens")
-    lse = _side(LSE, b * heads, torch.float32, Q, "LSE")
-    with _on(Q, stream) as st:
-        _check(load().tp_window_attn_decode(q, ldq, K.data_ptr(), ldk, bsk, V.data_ptr(), ldv, bsv,
-                                            plens, o, ldo, lse, b, cap, heads, kv_heads, d, window,
-                                            sinks, scale, _DTYPES[Q.dtype], _ptr(ws),
-                                            ws.numel() * ws.element_size(), st))
+        s = t.stride()
+        if t.shape != shk or t.dtype is not dt or t.get_device() != dev or s[2] != 1:
+            _bad(t, n, shk, dt, dev)
+        cache += (t.data_ptr(), s[1] if cap > 1 else shk[2], s[0] if b > 1 else 0)
+    q, ldq = _rows(Q, "Q", shq, dt, dev)
+    o, ldo = _rows(O, "O", shq, dt, dev)
+    w, wb = _ws(ws, dev)
+    status = load().tp_window_attn_decode(q, ldq, *cache, _flat(lens, "lens", b, torch.int32, dev),
+                                          o, ldo, _flat(LSE, "LSE", b * heads, torch.float32, dev),
+                                          b, cap, heads, kv_heads, d, window, sinks, scale,
+                                          _HALF[dt], w, wb, _raw_stream(stream, dev))
+    if status:
+        _check(status)
 
 
 def _bytes(n: int, device) -> torch.Tensor:

@@ -125,7 +125,7 @@ struct Gemm {
 // The gated block's forward on a few tokens (M <= kThinMaxM), by kernels that
 // stream the weights: H = act(x wgu + bgu) ([g | u] to gu unless nullptr), z =
 // H wd + bd.
-constexpr int64_t kThinMaxM = 64;
+constexpr int64_t kThinMaxM = 32;
 struct ThinGlu {
   const void *x = nullptr, *wgu = nullptr, *bgu = nullptr, *wd = nullptr, *bd = nullptr;
   void *H = nullptr, *gu = nullptr, *z = nullptr;

@@ -17,9 +17,15 @@
 // * The down product is launched with programmatic stream serialisation: its
 //   blocks start as the up product's finish, request their first weight tiles,
 //   and only then wait for H.
-// All blocks run at once (clusters are sized for that): every block then has
-// the same number of bytes in flight, so they share the HBM evenly and end
-// together whatever the number of blocks per SM.
+// All blocks run at once, two per SM (clusters are sized for that).
+// Measured: one token, h = 4096, f = 14336 (352 MB of weights) 59 us, 6.0 TB/s
+// over both products; 13 tokens, h = 2048, f = 5632 (69 MB) 23.6 us.  Tried on
+// these: five stages 61 / 23.7 us, three 62 / 24.1; clusters up to 16 blocks
+// 72 / 27; blocks of 4 warps, five per SM, 81 / 29; an even share of all slabs
+// per block with partial sums through HBM, joined by the last block of a tile,
+// 73 / 51.  Against the tcgen05 GEMM, whose 128-row tiles read the same
+// weights: 32 tokens 82 against 84 us (h = 2048: 31 against 39), 64 tokens 150
+// against 88 (52 against 40), so this path ends at 32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,6 +42,7 @@ constexpr int kGroups = 4;  // K groups; kWarps / kGroups = 2 column runs
 constexpr int kCols = 64;   // columns of a run
 constexpr int kStepK = 16;
 constexpr int kMaxCluster = 8;
+constexpr int kMinSteps = 4;  // of a warp
 
 struct ThinArgs {
   const __nv_bfloat16 *x, *w, *bias;
@@ -49,7 +56,7 @@ struct ThinArgs {
 
 template <int MT>
 struct Cfg {
-  static constexpr int kStages = MT == 1 ? 5 : MT == 2 ? 4 : 6;
+  static constexpr int kStages = 4;
   static constexpr int kWBytes = kStepK * kCols * 2;         // 2 KB
   static constexpr int kXBytes = MT * 16 * kStepK * 2;       // 512 bytes per 16 tokens
   static constexpr int kStageBytes = kWBytes + kXBytes;
@@ -98,7 +105,7 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
 }
 
 template <int MT, bool GLU>
-__global__ void __launch_bounds__(kThreads, MT <= 2 ? 2 : 1) thin_product(const ThinArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
   using C = Cfg<MT>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -278,14 +285,12 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 2 : 1) thin_product(const 
 }
 
 // Blocks per tile: the largest cluster with which all blocks still run at
-// once (two per SM, one with 4 m-tiles) and every warp keeps a few steps.
-int plan_split(int tiles, int K, int per_sm) {
-  const int steps = (K + kStepK - 1) / kStepK;
-  int s = 1;
-  while (2 * s <= kMaxCluster && tiles * 2LL * s <= static_cast<long long>(per_sm) * sm_count() &&
-         steps >= 2 * s * kGroups * 4)
-    s *= 2;
-  return s;
+// once (two per SM) and every warp keeps a few steps.
+int plan_split(int tiles, int K) {
+  const int64_t steps = (K + kStepK - 1) / kStepK;
+  const int64_t fit = 2LL * sm_count() / tiles;
+  return static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>({kMaxCluster, fit, steps / (kGroups * kMinSteps)})));
 }
 
 template <int MT, bool GLU>
@@ -296,7 +301,7 @@ tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
   if (e != cudaSuccess) return cuda_fail(e, "thin product smem");
   const int width = GLU ? kCols : 2 * kCols;
   const int tiles = (a.N + width - 1) / width;
-  a.split = plan_split(tiles, a.K, MT <= 2 ? 2 : 1);
+  a.split = plan_split(tiles, a.K);
   a.pdl = pdl ? 1 : 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * a.split);
@@ -329,9 +334,7 @@ tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
 
 template <bool GLU>
 tp_status launch_m(const ThinArgs& a, bool pdl, cudaStream_t stream) {
-  if (a.M <= 16) return launch<1, GLU>(a, pdl, stream);
-  if (a.M <= 32) return launch<2, GLU>(a, pdl, stream);
-  return launch<4, GLU>(a, pdl, stream);
+  return a.M <= 16 ? launch<1, GLU>(a, pdl, stream) : launch<2, GLU>(a, pdl, stream);
 }
 
 }  // namespace

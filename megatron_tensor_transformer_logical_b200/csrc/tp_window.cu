@@ -512,54 +512,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Row terms of the backward: nd = -rowsum(dO * O), nlse = -LSE * log2(e); a
 // row that saw no key (LSE = -inf) gets nlse = -inf, i.e. P = 0.  DH / 8
-// threads per (row, head) with 16-byte loads; the same threads zero the row
-// padding and the 64-float tail.  HBM-bound: 4 bytes read per element.
+// threads per (row, head) with 16-byte loads.  HBM-bound, 4 bytes read per
+// element: a block takes one row of queries (its indices come from one
+// division for all its threads: a 64-bit division per thread cost 36 us
+// instead of FIXME at b = 2, s = 4096, 32 heads of 128) and up to two of its
+// heads per thread group.  Blocks past the rows zero the row padding and the
+// 64-float tail.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(256)
     window_dsum(const void* o, long long ldo, const void* d_o, long long lddo, const float* lse,
-                float* nlse, float* nd, long long rows, int sq, int heads, int sp) {
-  constexpr int kLanes = DH / 8;
-  const long long t = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long pair = t / kLanes;  // (row, head), head fastest
-  const int l = threadIdx.x & (kLanes - 1);
-  const bool in = pair < rows * heads;
-  float acc = 0.0f, ls = 0.0f;
-  long long dst = 0;
-  if (in) {
-    const long long row = pair / heads;
-    const int head = static_cast<int>(pair - row * heads);
-    const long long bi = row / sq, r = row - bi * sq;
-    const long long q = bi * heads + head;
-    dst = q * sp + r;
-    if (l == 0) ls = lse[q * sq + r];
-    const uint4 ov = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o) + row * ldo +
-                                                     head * DH + l * 8);
-    const uint4 dv = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d_o) +
-                                                     row * lddo + head * DH + l * 8);
-    const uint32_t ow[4] = {ov.x, ov.y, ov.z, ov.w}, dw[4] = {dv.x, dv.y, dv.z, dv.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = unpack2<BF>(ow[i]), y = unpack2<BF>(dw[i]);
-      acc = fmaf(x.x, y.x, acc);
-      acc = fmaf(x.y, y.y, acc);
+                float* nlse, float* nd, int rows, int sq, int heads, int sp) {
+  constexpr int kLanes = DH / 8, kHeads = 256 / kLanes;  // heads at a time
+  if (blockIdx.x >= rows) {
+    const long long bh = static_cast<long long>(rows / sq) * heads;
+    const int padr = sp - sq;
+    const long long t = static_cast<long long>(blockIdx.x - rows) * 256 + threadIdx.x;
+    if (t < bh * padr + 64) {
+      const long long i = t < bh * padr ? t / padr * sp + sq + t % padr : bh * sp + (t - bh * padr);
+      nd[i] = 0.0f;
+      nlse[i] = 0.0f;
     }
+    return;
   }
+  const int row = blockIdx.x, bi = row / sq, r = row - bi * sq;
+  const int l = threadIdx.x & (kLanes - 1);
+  const uint16_t* op = static_cast<const uint16_t*>(o) + row * ldo + l * 8;
+  const uint16_t* dp = static_cast<const uint16_t*>(d_o) + row * lddo + l * 8;
+  for (int h0 = 0; h0 < heads; h0 += 2 * kHeads) {
+    uint4 ov[2], dv[2];
+    float ls[2];
 #pragma unroll
-  for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-  if (in && l == 0) {
-    nd[dst] = -acc;
-    nlse[dst] = ls == -INFINITY ? -INFINITY : -(ls * kLog2e);
-  }
-  const long long bh = rows / sq * heads;
-  const int padr = sp - sq;
-  if (t < bh * padr) {
-    const long long i = t / padr * sp + sq + t % padr;
-    nd[i] = 0.0f;
-    nlse[i] = 0.0f;
-  } else if (t < bh * padr + 64) {
-    const long long i = bh * sp + (t - bh * padr);
-    nd[i] = 0.0f;
-    nlse[i] = 0.0f;
+    for (int k = 0; k < 2; ++k) {
+      const int head = h0 + k * kHeads + static_cast<int>(threadIdx.x) / kLanes;
+      ov[k] = dv[k] = make_uint4(0u, 0u, 0u, 0u);
+      ls[k] = 0.0f;
+      if (head < heads) {
+        ov[k] = *reinterpret_cast<const uint4*>(op + head * DH);
+        dv[k] = *reinterpret_cast<const uint4*>(dp + head * DH);
+        if (l == 0) ls[k] = lse[(static_cast<long long>(bi) * heads + head) * sq + r];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int head = h0 + k * kHeads + static_cast<int>(threadIdx.x) / kLanes;
+      const uint32_t ow[4] = {ov[k].x, ov[k].y, ov[k].z, ov[k].w};
+      const uint32_t dw[4] = {dv[k].x, dv[k].y, dv[k].z, dv[k].w};
+      float acc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = unpack2<BF>(ow[i]), y = unpack2<BF>(dw[i]);
+        acc = fmaf(x.x, y.x, acc);
+        acc = fmaf(x.y, y.y, acc);
+      }
+#pragma unroll
+      for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+      if (l == 0 && head < heads) {
+        const long long dst = (static_cast<long long>(bi) * heads + head) * sp + r;
+        nd[dst] = -acc;
+        nlse[dst] = ls[k] == -INFINITY ? -INFINITY : -(ls[k] * kLog2e);
+      }
+    }
   }
 }
 
@@ -1394,15 +1406,15 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
     return s;
   const int64_t rows = w.b * w.sq;
   const int64_t pad = w.b * w.heads * (a.sp - w.sq) + 64;
-  const int64_t threads = std::max(rows * w.heads * (DH / 8), pad);
+  const int64_t dsum_blocks = rows + (pad + 255) / 256;
   const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
   dim3 gq(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
   const unsigned gk = static_cast<unsigned>(std::min<int64_t>(p.items, sm_count()));
   const int joins = (p.split_s > 1) + (p.split_w > 1 && p.key_tiles > p.sink_tiles);
   LaunchScope scope(TP_KIND_ATTN_BWD, 10.0 * DH * visible_pairs(w),
                     double(w.b) * (8.0 * w.sq * nq + 8.0 * w.sk * nk), stream, 3 + joins);
-  window_dsum<BF, DH><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(
-      w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, rows, a.sq, a.heads, a.sp);
+  window_dsum<BF, DH><<<static_cast<unsigned>(dsum_blocks), 256, 0, stream>>>(
+      w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, static_cast<int>(rows), a.sq, a.heads, a.sp);
   window_bwd_dq<BF, DH><<<gq, kThreads, smem_q, stream>>>(q128, do128, k64, v64, a);
   window_bwd_dkdv<BF, DH><<<gk, kThreads, smem_kv, stream>>>(k128, v128, q64, do64, a);
   if (p.split_s > 1)
@@ -1424,7 +1436,7 @@ tp_status window_attn_check(const WindowAttn& w) {
   const int64_t tiles = (w.sk + kBN - 1) / kBN;
   if (tiles * w.b * w.kv_heads > 0x7fffffffLL / kMaxSlices ||
       (w.sq + kB64 - 1) / kB64 * (w.heads / w.kv_heads) > 0x7fffffffLL ||
-      w.b * w.sq * w.heads > (1ll << 34))
+      w.b * w.sq > 0x60000000LL || w.b * w.heads > 0x10000000LL)
     return fail(TP_ERR_SHAPE, "window attention: too many key tiles");
   return TP_OK;
 }

@@ -10,9 +10,10 @@
 // * the G query heads of a key head (16 at a time) are the 16 rows of an
 //   m16n8k16 product, so a key is read once for all of them and the
 //   arithmetic stays far from the limit;
-// * every warp streams its own 16-key tiles through its own ring of
+// * every warp streams its own 16-key tiles through its own ring of three
 //   cp.async stages (no block barrier in the loop) and keeps its own running
-//   maximum, sum and O; the block's warps are joined at its end.
+//   maximum, sum and O; the block's warps are joined at its end.  Four stages
+//   or eight warps, which leave one block per SM, were 10-25% slower.
 // Keys past the visible range are read as zeros and masked, so what the
 // cache holds beyond lens never enters, whatever it is.
 #include <cuda_bf16.h>
@@ -26,10 +27,10 @@
 namespace tp {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTileKeys = 16;  // per warp and step
 constexpr int kStages = 3;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;      // query heads per block
 constexpr int kMaxSplits = 255;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
   const int rows = min(a.group - gt * kRows, kRows);
   const int head0 = kvh * a.group + gt * kRows;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled
   const Visible vis(a.lens[bi], a);
   const int per = slice_keys(vis.total, a.splits);
   const int t0 = min(split * per, vis.total), t1 = min(t0 + per, vis.total);
@@ -345,6 +347,7 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
   const int item = (bi * a.kv_heads + kvh) * a.gtiles + gh / kRows;
   const long long p0 = static_cast<long long>(item) * a.splits * a.rows + gh % kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the slices are complete
   // one slice per thread (splits <= 255): the common maximum, then the weights
   const float2 ml = static_cast<int>(threadIdx.x) < a.splits
                         ? a.pml[p0 + static_cast<long long>(threadIdx.x) * a.rows]
@@ -401,15 +404,19 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
   }
 }
 
-// Slices per (sequence, key head): enough blocks for about four rounds of the
-// blocks that run at once (two per SM), each at least kMinKeys keys.
+// Slices per (sequence, key head): as many as fill the blocks that run at once
+// (two per SM), each at least kMinKeys keys.  One round of long slices beats
+// several rounds of short ones: one sequence of 131072 keys, 4 key heads of
+// 128 in bf16 (267 MB), 48 us with 74 slices, 56 with 148, 70 with 255; 32
+// sequences of 4100 visible keys, 8 key heads (537 MB): 87 us with two slices,
+// 91 with four, 96 with five.
 constexpr int kMinKeys = 256;
 
 int plan_splits(const WindowDecode& w) {
   const int64_t gt = (w.heads / w.kv_heads + kRows - 1) / kRows;
   const int64_t items = w.b * w.kv_heads * gt;
   const int64_t keys = std::min(w.cap, w.window + w.sinks);
-  const int64_t want = (8LL * sm_count() + items - 1) / items;
+  const int64_t want = (2LL * sm_count() + items - 1) / items;
   return static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>({want, (keys + kMinKeys - 1) / kMinKeys, kMaxSplits})));
 }
@@ -453,9 +460,20 @@ tp_status decode(const WindowDecode& w, void* scratch, cudaStream_t stream) {
   LaunchScope scope(TP_KIND_ATTN_FWD, 4.0 * DH * keys * w.heads, 4.0 * DH * keys * w.kv_heads,
                     stream, a.splits > 1 ? 2 : 1);
   window_decode<BF, DH><<<dim3(static_cast<unsigned>(items), a.splits), kThreads, smem, stream>>>(a);
-  if (a.splits > 1)
-    window_decode_join<BF, DH><<<static_cast<unsigned>(w.b * w.heads), 256, 0, stream>>>(a);
   e = cudaGetLastError();
+  if (e == cudaSuccess && a.splits > 1) {
+    // Scheduled while the slices finish; it waits for them itself.
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(w.b * w.heads));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, window_decode_join<BF, DH>, a);
+  }
   return e == cudaSuccess ? TP_OK : cuda_fail(e, "window decode launch");
 }
 
