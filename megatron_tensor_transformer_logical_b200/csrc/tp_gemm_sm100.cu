@@ -1582,7 +1582,8 @@ double est_tiles(const Gemm& g, long long T, int workers, size_t part_bytes, dou
 // faster than the pair; with both operands MN-major (wgrads) the pair is
 // 6-12% faster; with both K-major (dgrads) the single-SM tile is 3-6% faster
 // in natural K order and the pair 7% faster in the attention's head-group K
-// order.  The 192- and 128-wide tiles run 15% and 30% slower per tile and
+// order; with the gated gradient's epilogue the pair is 6% faster (4096 x 14336
+// x 4096: 403 against 429 us).  The 192- and 128-wide tiles run 15% and 30% slower per tile and
 // only pay where they fill the last wave far better.  With at most 16 K
 // blocks the per-tile epilogue, not the main loop, sets the pace and the
 // narrower tiles lose only 4% and 10% (workload 2's K = 768 GEMMs: 60 us on
@@ -1611,6 +1612,8 @@ int choose_tile(const Gemm& g) {
   double pair_rate;
   if (g.a.k_major && !g.b.k_major)
     pair_rate = 0.96;                                 // forward
+  else if (g.epi == kEpiDGlu)
+    pair_rate = 1.05;  // its operand and three outputs leave less L2 to the B tiles
   else if (g.a.k_major && g.b.k_major)
     pair_rate = g.korder.range_blocks > 0 ? 1.07 : 0.96;  // dgrad
   else

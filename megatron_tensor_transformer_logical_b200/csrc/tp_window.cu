@@ -33,7 +33,14 @@
 //
 // bf16 and fp16 inputs; P and dS are rounded to the input type for their
 // products (fp32 accumulation), as the products take one type for both
-// operands.
+// operands.  In the backward, queries that see at most kSplitKeys keys give P
+// and dS as two terms, the rounded value and the rounded rest, and the
+// products take both (whole query tiles, and in dK / dV whole key tiles): with
+// few keys the row term D, taken from the rounded O,
+// already costs as much accuracy as the results' own rounding, and the
+// rounding of dS would come on top (gradients 1.5-1.8 times as far from exact
+// as their rounding alone, 1.1-1.4 times with the two terms).  Rows with many
+// keys average both out.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,6 +49,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attn_sm100.cuh"
 #include "ptx_sm100.cuh"
@@ -56,6 +64,7 @@ constexpr int kB64 = 64;  // keys per block (dQ), queries per block (dK / dV)
 constexpr int kThreads = 384;
 constexpr float kRescaleLog2 = 8.0f;  // O keeps a stale maximum up to 2^8 behind
 constexpr float kCheckSum = 255.0f;   // a row sum above this may hide such a key
+constexpr int kSplitKeys = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -78,6 +87,14 @@ template <bool BF>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   if (BF) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Two values as the rounded pair and the rounded rest.
+template <bool BF>
+__device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
+  hi = pack2<BF>(v.x, v.y);
+  const float2 h = unpack2<BF>(hi);
+  lo = pack2<BF>(v.x - h.x, v.y - h.y);
 }
 
 // Eight fp32 values as one 16-byte store of the input type.
@@ -157,6 +174,14 @@ struct BlockList {
     return xhi < 0 ? 0 : xhi + 1 - max(0, xlo - nsb);
   }
 };
+
+// Whether queries in general see at most kSplitKeys keys (by the window), so
+// that P and dS are given in two terms everywhere.  Otherwise those at the
+// first kSplitKeys positions do, which are the ones that see the first keys
+// only.
+__device__ __forceinline__ bool split_all(const WinArgs& a) {
+  return a.window <= kSplitKeys - a.sinks;
+}
 
 // Visible columns of a row within one key block: [0, end) intersected with
 // [first, inf) or [0, sink).
@@ -243,6 +268,13 @@ __device__ __forceinline__ float exp_row_masked(uint32_t srow, const RowMask& ma
   }
   return acc.x + acc.y;
 }
+
+// Programmatic launches: lets the next kernel of the stream be scheduled; and
+// waits until the kernels before this one are complete.
+__device__ __forceinline__ void pdl_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // One box per 64 columns of a [rows x DH] tile; the halves are rows * 128
 // bytes apart.
@@ -512,65 +544,67 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Row terms of the backward: nd = -rowsum(dO * O), nlse = -LSE * log2(e); a
 // row that saw no key (LSE = -inf) gets nlse = -inf, i.e. P = 0.  DH / 8
-// threads per (row, head) with 16-byte loads.  HBM-bound, 4 bytes read per
-// element: a block takes one row of queries (its indices come from one
-// division for all its threads: a 64-bit division per thread cost 36 us
-// instead of FIXME at b = 2, s = 4096, 32 heads of 128) and up to two of its
-// heads per thread group.  Blocks past the rows zero the row padding and the
-// 64-float tail.
+// threads per (row, head) with 16-byte loads, two pairs in flight.  HBM-bound,
+// 4 bytes read per element: 24 us at b = 2, s = 4096, 32 heads of 128 (134
+// MB); with 64-bit divisions for the indices the same loop took 36 us.  Blocks
+// past the rows zero the row padding and the 64-float tail.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(256)
     window_dsum(const void* o, long long ldo, const void* d_o, long long lddo, const float* lse,
-                float* nlse, float* nd, int rows, int sq, int heads, int sp) {
-  constexpr int kLanes = DH / 8, kHeads = 256 / kLanes;  // heads at a time
-  if (blockIdx.x >= rows) {
-    const long long bh = static_cast<long long>(rows / sq) * heads;
+                float* nlse, float* nd, unsigned pairs, unsigned blocks, unsigned bh, int sq,
+                unsigned heads, int sp) {
+  constexpr int kLanes = DH / 8, kGroups = 256 / kLanes;
+  pdl_next();
+  if (blockIdx.x >= blocks) {
     const int padr = sp - sq;
-    const long long t = static_cast<long long>(blockIdx.x - rows) * 256 + threadIdx.x;
-    if (t < bh * padr + 64) {
-      const long long i = t < bh * padr ? t / padr * sp + sq + t % padr : bh * sp + (t - bh * padr);
+    const long long t = static_cast<long long>(blockIdx.x - blocks) * 256 + threadIdx.x;
+    const long long n = static_cast<long long>(bh) * padr;
+    if (t < n + 64) {
+      const long long i =
+          t < n ? t / padr * sp + sq + t % padr : static_cast<long long>(bh) * sp + (t - n);
       nd[i] = 0.0f;
       nlse[i] = 0.0f;
     }
     return;
   }
-  const int row = blockIdx.x, bi = row / sq, r = row - bi * sq;
   const int l = threadIdx.x & (kLanes - 1);
-  const uint16_t* op = static_cast<const uint16_t*>(o) + row * ldo + l * 8;
-  const uint16_t* dp = static_cast<const uint16_t*>(d_o) + row * lddo + l * 8;
-  for (int h0 = 0; h0 < heads; h0 += 2 * kHeads) {
-    uint4 ov[2], dv[2];
-    float ls[2];
+  uint4 ov[2], dv[2];
+  float ls[2];
+  long long dst[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int head = h0 + k * kHeads + static_cast<int>(threadIdx.x) / kLanes;
-      ov[k] = dv[k] = make_uint4(0u, 0u, 0u, 0u);
-      ls[k] = 0.0f;
-      if (head < heads) {
-        ov[k] = *reinterpret_cast<const uint4*>(op + head * DH);
-        dv[k] = *reinterpret_cast<const uint4*>(dp + head * DH);
-        if (l == 0) ls[k] = lse[(static_cast<long long>(bi) * heads + head) * sq + r];
-      }
+  for (int k = 0; k < 2; ++k) {
+    const unsigned pair = (blockIdx.x * 2 + k) * kGroups + threadIdx.x / kLanes;  // head fastest
+    ov[k] = dv[k] = make_uint4(0u, 0u, 0u, 0u);
+    ls[k] = 0.0f;
+    dst[k] = -1;
+    if (pair < pairs) {
+      const unsigned row = pair / heads, head = pair - row * heads;
+      const unsigned bi = row / static_cast<unsigned>(sq), r = row - bi * sq;
+      const long long q = static_cast<long long>(bi) * heads + head;
+      ov[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(o) + row * ldo +
+                                              head * DH + l * 8);
+      dv[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(d_o) + row * lddo +
+                                              head * DH + l * 8);
+      if (l == 0) ls[k] = lse[q * sq + r];
+      dst[k] = q * sp + r;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t ow[4] = {ov[k].x, ov[k].y, ov[k].z, ov[k].w};
+    const uint32_t dw[4] = {dv[k].x, dv[k].y, dv[k].z, dv[k].w};
+    float acc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2<BF>(ow[i]), y = unpack2<BF>(dw[i]);
+      acc = fmaf(x.x, y.x, acc);
+      acc = fmaf(x.y, y.y, acc);
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int head = h0 + k * kHeads + static_cast<int>(threadIdx.x) / kLanes;
-      const uint32_t ow[4] = {ov[k].x, ov[k].y, ov[k].z, ov[k].w};
-      const uint32_t dw[4] = {dv[k].x, dv[k].y, dv[k].z, dv[k].w};
-      float acc = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 x = unpack2<BF>(ow[i]), y = unpack2<BF>(dw[i]);
-        acc = fmaf(x.x, y.x, acc);
-        acc = fmaf(x.y, y.y, acc);
-      }
-#pragma unroll
-      for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
-      if (l == 0 && head < heads) {
-        const long long dst = (static_cast<long long>(bi) * heads + head) * sp + r;
-        nd[dst] = -acc;
-        nlse[dst] = ls[k] == -INFINITY ? -INFINITY : -(ls[k] * kLog2e);
-      }
+    for (int s = kLanes / 2; s > 0; s >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, s);
+    if (l == 0 && dst[k] >= 0) {
+      nd[dst[k]] = -acc;
+      nlse[dst[k]] = ls[k] == -INFINITY ? -INFINITY : -(ls[k] * kLog2e);
     }
   }
 }
@@ -614,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kvh = head / a.group;
   const int r0 = 2 * pair * kBM;
   const BlockList<kB64> bl(r0, a);
+  const bool two_terms = split_all(a) || r0 + 2 * kBM + a.off <= kSplitKeys;
 
   if (threadIdx.x == 0) {
     mbar_init(qd_full, 1);
@@ -636,8 +671,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_next();
+  pdl_wait();  // the row terms
   // Tile x: S_x at [256 x, +64) (dS_x over its first 32 columns), dP_x at
-  // [256 x + 64, +64), dQ_x at [256 x + 128, + DH).
+  // [256 x + 64, +64) (the rest of dS_x over its first 32 columns, if taken),
+  // dQ_x at [256 x + 128, + DH).
   auto tS = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x); };
   auto tP = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 64); };
   auto tQ = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
@@ -686,40 +724,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int total[2] = {bl.count(0), bl.count(1)};
       int done[2] = {0, 0};
       bool ok = mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
-      for (int j = -1; j < bl.n && ok; ++j) {
-        const bool more = j + 1 < bl.n;
-        bool kv_next = false;
+      auto issue = [&](auto two) {
+        for (int j = -1; j < bl.n && ok; ++j) {
+          const bool more = j + 1 < bl.n;
+          bool kv_next = false;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok) break;
-          if (j >= 0 && bl.sees(x, j)) {
-            if (!(ok = mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
-                                 kStatusAttnTimeout)))
-              break;
-            tc_fence_after();
-            const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
-#pragma unroll
-            for (int kk = 0; kk < kB64 / 16; ++kk)
-              umma_f16_ts(tQ(x), tS(x) + static_cast<uint32_t>(kk * 8),
-                          sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ,
-                          (done[x] > 0 || kk > 0) ? 1u : 0u);
-            if (++done[x] == total[x]) umma_commit(&dq_done[x]);
-          }
-          if (more && bl.sees(x, j + 1)) {
-            if (!kv_next) {
-              const int ks = (j + 1) % kKvStages;
-              if (!(ok = mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
-                                   a.status, kStatusAttnTimeout)))
+          for (int x = 0; x < 2; ++x) {
+            if (!ok) break;
+            if (j >= 0 && bl.sees(x, j)) {
+              if (!(ok = mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
+                                   kStatusAttnTimeout)))
                 break;
               tc_fence_after();
-              kv_next = true;
+              const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
+#pragma unroll
+              for (int kk = 0; kk < kB64 / 16; ++kk)
+                umma_f16_ts(tQ(x), tS(x) + static_cast<uint32_t>(kk * 8),
+                            sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ,
+                            (done[x] > 0 || kk > 0) ? 1u : 0u);
+              if constexpr (two) {
+#pragma unroll
+                for (int kk = 0; kk < kB64 / 16; ++kk)
+                  umma_f16_ts(tQ(x), tP(x) + static_cast<uint32_t>(kk * 8),
+                              sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ, 1u);
+              }
+              if (++done[x] == total[x]) umma_commit(&dq_done[x]);
             }
-            issue_sp(x, j + 1);
+            if (more && bl.sees(x, j + 1)) {
+              if (!kv_next) {
+                const int ks = (j + 1) % kKvStages;
+                if (!(ok = mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
+                                     a.status, kStatusAttnTimeout)))
+                  break;
+                tc_fence_after();
+                kv_next = true;
+              }
+              issue_sp(x, j + 1);
+            }
           }
+          if (!ok) break;
+          if (j >= 0) umma_commit(&kv_empty[j % kKvStages]);
         }
-        if (!ok) break;
-        if (j >= 0) umma_commit(&kv_empty[j % kKvStages]);
-      }
+      };
+      if (two_terms)
+        issue(std::true_type{});
+      else
+        issue(std::false_type{});
     }
   } else if (warp >= 4) {
     const int x = (warp - 4) >> 2;
@@ -734,47 +784,66 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p = rc + a.off;
     const int total = bl.count(x);
     bool ok = true;
-    int cnt = 0;
-    for (int j = 0; j < bl.n && cnt < total; ++j) {
-      if (!bl.sees(x, j)) continue;
-      if (!(ok = mbar_wait(&s_full[x], static_cast<uint32_t>(cnt) & 1u, a.status,
-                           kStatusAttnTimeout)))
-        break;
-      tc_fence_after();
-      const RowMask mask = row_mask(p, bl.block(j) * kB64, a);
+    // One loop for tiles that give dS in two terms, one for the others.
+    auto blocks = [&](auto two) {
+      int cnt = 0;
+      for (int j = 0; j < bl.n && cnt < total; ++j) {
+        if (!bl.sees(x, j)) continue;
+        if (!(ok = mbar_wait(&s_full[x], static_cast<uint32_t>(cnt) & 1u, a.status,
+                             kStatusAttnTimeout)))
+          break;
+        tc_fence_after();
+        const RowMask mask = row_mask(p, bl.block(j) * kB64, a);
 #pragma unroll
-      for (int c = 0; c < kB64; c += 32) {
-        float sv[32], pv[32];
-        tmem_ld32x2(tS(x) + lane_off + c, sv, tP(x) + lane_off + c, pv);
-        uint32_t pk[16];
-        const uint32_t vis = mask.full(c) ? 0xffffffffu : mask.bits(c);
-        if (vis == 0xffffffffu) {
+        for (int c = 0; c < kB64; c += 32) {
+          float sv[32], pv[32];
+          tmem_ld32x2(tS(x) + lane_off + c, sv, tP(x) + lane_off + c, pv);
+          uint32_t pk[16];
+          const uint32_t vis = mask.full(c) ? 0xffffffffu : mask.bits(c);
+          // dS = P (dP - D), two entries at a time.
+          if constexpr (two) {
+            uint32_t lk[16];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
-            const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-            const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
-            pk[i >> 1] = pack2<BF>(g.x, g.y);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
+              const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
+                                           (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
+              const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              split2<BF>(g, pk[i >> 1], lk[i >> 1]);
+            }
+            tmem_st16(tP(x) + lane_off + c / 2, lk);
+          } else if (vis == 0xffffffffu) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
+              const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              pk[i >> 1] = pack2<BF>(g.x, g.y);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
+              const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
+                                           (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
+              const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              pk[i >> 1] = pack2<BF>(g.x, g.y);
+            }
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
-            const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
-                                         (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
-            const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
-            pk[i >> 1] = pack2<BF>(g.x, g.y);
-          }
+          // dS columns [c / 2, c / 2 + 16): columns this thread has read.
+          tmem_st16(tS(x) + lane_off + c / 2, pk);
         }
-        // dS columns [c / 2, c / 2 + 16): S columns this thread has read.
-        tmem_st16(tS(x) + lane_off + c / 2, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ds_full[x]);
+        ++cnt;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ds_full[x]);
-      ++cnt;
-    }
+    };
+    if (two_terms)
+      blocks(std::true_type{});
+    else
+      blocks(std::false_type{});
     if (ok && total > 0) ok = mbar_wait(&dq_done[x], 0, a.status, kStatusAttnTimeout);
     if (ok) {
       if (total > 0) tc_fence_after();
@@ -842,6 +911,7 @@ __host__ __device__ __forceinline__ QRange query_blocks(int k0, int sq, int sk, 
 struct KvItem {
   int bi, kvh, k0, i0, n, j0, j1;
   int slot;  // slice of the partials, -1: the tile is not cut
+  bool two;  // P and dS in two terms
 };
 
 __device__ __forceinline__ KvItem kv_item(int k, const WinArgs& a) {
@@ -868,6 +938,7 @@ __device__ __forceinline__ KvItem kv_item(int k, const WinArgs& a) {
   it.kvh = bk % a.kv_heads;
   it.bi = bk / a.kv_heads;
   it.k0 = kb * kBN;
+  it.two = split_all(a) || it.k0 < kSplitKeys;
   const QRange q = query_blocks(it.k0, a.sq, a.sk, a.window, a.sinks);
   it.i0 = q.i0;
   it.n = q.n;
@@ -892,8 +963,10 @@ __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
 // (acc_empty).  Items without queries only write zeros.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
-    window_bwd_dkdv(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+    window_bwd_dkdv(const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV,
+                    const __grid_constant__ CUtensorMap tmQ,
+                    const __grid_constant__ CUtensorMap tmdO,
                     const WinArgs a) {
   constexpr int kTile = KvSmem<DH>::kTile, kTile64 = KvSmem<DH>::kTile64;
   constexpr int kEwWarps = 8;
@@ -941,6 +1014,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_next();
+  pdl_wait();  // the row terms
   // S^T buffers at columns 0 and 64, dP^T at 128 and 192, dV at 256, dK at 384.
   auto tS = [tmem](int st) { return tmem + static_cast<uint32_t>(64 * st); };
   auto tP = [tmem](int st) { return tmem + static_cast<uint32_t>(128 + 64 * st); };
@@ -1027,37 +1102,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait(kv_full, it_no & 1u, a.status, kStatusAttnTimeout))) break;
         if (!(ok = issue_sp(g))) break;
         if (len == 1) umma_commit(kv_empty);
-        for (int j = 0; j < len; ++j) {
-          const long long gj = g + j;
-          if (j + 1 < len) {
-            if (!(ok = issue_sp(gj + 1))) break;
-            if (j + 2 == len) umma_commit(kv_empty);  // the item's last S^T / dP^T
-          }
-          const int st = static_cast<int>(gj & 1);
-          if (!(ok = mbar_wait(&p_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
-                               kStatusAttnTimeout)))
-            break;
-          // The item's first products overwrite the accumulators: the previous
-          // item's epilogue must have read them.
-          if (j == 0 && it_no > 0 &&
-              !(ok = mbar_wait(acc_empty, (it_no - 1u) & 1u, a.status, kStatusAttnTimeout)))
-            break;
-          tc_fence_after();
-          const int qs = static_cast<int>(gj % kQdStages);
-          const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
-          const uint32_t do_addr = q_addr + kTile64;
+        auto issue = [&](auto two) {
+          for (int j = 0; j < len; ++j) {
+            const long long gj = g + j;
+            if (j + 1 < len) {
+              if (!(ok = issue_sp(gj + 1))) break;
+              if (j + 2 == len) umma_commit(kv_empty);  // the item's last S^T / dP^T
+            }
+            const int st = static_cast<int>(gj & 1);
+            if (!(ok = mbar_wait(&p_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+                                 kStatusAttnTimeout)))
+              break;
+            // The item's first products overwrite the accumulators: the previous
+            // item's epilogue must have read them.
+            if (j == 0 && it_no > 0 &&
+                !(ok = mbar_wait(acc_empty, (it_no - 1u) & 1u, a.status, kStatusAttnTimeout)))
+              break;
+            tc_fence_after();
+            const int qs = static_cast<int>(gj % kQdStages);
+            const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
+            const uint32_t do_addr = q_addr + kTile64;
 #pragma unroll
-          for (int kk = 0; kk < kB64 / 16; ++kk) {
-            // queries [16 kk, 16 kk + 16): group kk / 2's columns, 8 columns each
-            const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
-            const uint32_t acc = (j | kk) != 0 ? 1u : 0u;
-            umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
-                        kIdAcc, acc);
-            umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
-                        kIdAcc, acc);
+            for (int kk = 0; kk < kB64 / 16; ++kk) {
+              // queries [16 kk, 16 kk + 16): group kk / 2's columns, 8 columns each
+              const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
+              const uint32_t acc = (j | kk) != 0 ? 1u : 0u;
+              umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
+                          kIdAcc, acc);
+              umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
+                          kIdAcc, acc);
+            }
+            if constexpr (two) {
+              // the second terms, 16 columns on
+#pragma unroll
+              for (int kk = 0; kk < kB64 / 16; ++kk) {
+                const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1) + 16);
+                umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
+                            kIdAcc, 1u);
+                umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
+                            kIdAcc, 1u);
+              }
+            }
+            umma_commit(&qd_empty[qs]);
           }
-          umma_commit(&qd_empty[qs]);
-        }
+        };
+        if (it.two)
+          issue(std::true_type{});
+        else
+          issue(std::false_type{});
         if (!ok) break;
         umma_commit(acc_done);
         g += len;
@@ -1088,52 +1180,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    static_cast<long long>(key) + a.window - a.off));
       if (key >= a.sk) qhi = 0;
       int qi = it.n > 0 ? it.j0 % it.n : 0;
-      for (int j = 0; j < len; ++j) {
-        const long long gj = gb + j;
-        const int st = static_cast<int>(gj & 1);
-        const int qs = static_cast<int>(gj % kQdStages);
-        const int q0 = (it.i0 + qi) * kB64;
-        if (++qi == it.n) qi = 0;
-        if (!(ok = mbar_wait(&s_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
-                             kStatusAttnTimeout)))
-          break;
-        // The block's row terms were staged with its Q / dO; the stage cannot
-        // be refilled before this block's products are done.
-        if (!(ok = mbar_wait(&qd_full[qs], static_cast<uint32_t>(gj / kQdStages) & 1u, a.status,
-                             kStatusAttnTimeout)))
-          break;
-        tc_fence_after();
-        const float* wstat = s_stat + qs * (2 * kB64) + c;
-        const int lo = qlo - q0 - c, hi = qhi - q0 - c;  // visible columns lo <= i < hi
-        float sv[32], pv[32];
-        tmem_ld32x2(tS(st) + lane_off + c, sv, tP(st) + lane_off + c, pv);
-        uint32_t pk[16], dk[16];
-        const bool full = lo <= 0 && hi >= 32;
-        const uint32_t vis = full ? 0xffffffffu : RowMask::prefix(hi) & ~RowMask::prefix(lo);
+      auto blocks = [&](auto two) {
+        for (int j = 0; j < len; ++j) {
+          const long long gj = gb + j;
+          const int st = static_cast<int>(gj & 1);
+          const int qs = static_cast<int>(gj % kQdStages);
+          const int q0 = (it.i0 + qi) * kB64;
+          if (++qi == it.n) qi = 0;
+          if (!(ok = mbar_wait(&s_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+                               kStatusAttnTimeout)))
+            break;
+          // The block's row terms were staged with its Q / dO; the stage cannot
+          // be refilled before this block's products are done.
+          if (!(ok = mbar_wait(&qd_full[qs], static_cast<uint32_t>(gj / kQdStages) & 1u, a.status,
+                               kStatusAttnTimeout)))
+            break;
+          tc_fence_after();
+          const float* wstat = s_stat + qs * (2 * kB64) + c;
+          const int lo = qlo - q0 - c, hi = qhi - q0 - c;  // visible columns lo <= i < hi
+          float sv[32], pv[32];
+          tmem_ld32x2(tS(st) + lane_off + c, sv, tP(st) + lane_off + c, pv);
+          uint32_t pk[16], dk[16];
+          const bool full = lo <= 0 && hi >= 32;
+          const uint32_t vis = full ? 0xffffffffu : RowMask::prefix(hi) & ~RowMask::prefix(lo);
+          if constexpr (two) {
+            uint32_t pl[16], dl[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
-          const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
-          const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
-          float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-          float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
-          if (!full) {
-            // hidden queries may stand on the row terms of another sequence
-            const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
-            p = make_float2(v0 ? p.x : 0.0f, v1 ? p.y : 0.0f);
-            d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
+              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
+              float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
+              const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
+              const float2 p =
+                make_float2(v0 ? ex2_approx(t.x) : 0.0f, v1 ? ex2_approx(t.y) : 0.0f);
+              d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
+              split2<BF>(p, pk[i >> 1], pl[i >> 1]);
+              split2<BF>(__fmul2_rn(p, d), dk[i >> 1], dl[i >> 1]);
+            }
+            tmem_st16(tS(st) + lane_off + c + 16, pl);
+            tmem_st16(tP(st) + lane_off + c + 16, dl);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
+              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
+              float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
+              if (!full) {
+                // hidden queries may stand on the row terms of another sequence
+                const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
+                p = make_float2(v0 ? p.x : 0.0f, v1 ? p.y : 0.0f);
+                d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
+              }
+              pk[i >> 1] = pack2<BF>(p.x, p.y);
+              const float2 g = __fmul2_rn(p, d);
+              dk[i >> 1] = pack2<BF>(g.x, g.y);
+            }
           }
-          pk[i >> 1] = pack2<BF>(p.x, p.y);
-          const float2 g = __fmul2_rn(p, d);
-          dk[i >> 1] = pack2<BF>(g.x, g.y);
+          tmem_st16(tS(st) + lane_off + c, pk);  // P^T over this group's S^T columns
+          tmem_st16(tP(st) + lane_off + c, dk);  // dS^T over its dP^T columns
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[st]);
         }
-        tmem_st16(tS(st) + lane_off + c, pk);  // P^T over this group's S^T columns
-        tmem_st16(tP(st) + lane_off + c, dk);  // dS^T over its dP^T columns
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[st]);
-      }
+      };
+      if (it.two)
+        blocks(std::true_type{});
+      else
+        blocks(std::false_type{});
       if (!ok) break;
       if (len > 0) {
         gb += len;
@@ -1194,13 +1311,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool BF, int DH>
 __global__ void __launch_bounds__(128) window_kv_join(const WinArgs a, int first_tile, int split,
                                                       int slot0) {
+  pdl_next();
+  pdl_wait();  // the partials
   const int bk = blockIdx.x % a.bkv, kb = blockIdx.x / a.bkv;  // kb: among the class's tiles
   const int c8 = blockIdx.y, which = blockIdx.z;
   const int kvh = bk % a.kv_heads, bi = bk / a.kv_heads;
   const int key = (first_tile + kb) * kBN + threadIdx.x;
   if (key >= a.sk) return;
   const float4* p = reinterpret_cast<const float4*>(a.part) +
-                    (static_cast<long long>(slot0) + static_cast<long long>(kb * a.bkv + bk) * split) *
+                    (static_cast<long long>(slot0) +
+                     static_cast<long long>(kb * a.bkv + bk) * split) *
                         (2 * 128 * (DH / 4)) +
                     which * 128 * (DH / 4) + c8 * 2 * 128 + threadIdx.x;
   float v[8];
@@ -1285,7 +1405,8 @@ KvPlan plan_kv(const WindowAttn& w) {
   const int64_t share = blocks * bkv / (2 * sm_count());
   const int64_t slice = std::max<int64_t>(kMinSlice, share);
   auto cut = [&](int64_t n) {
-    return static_cast<int>(std::min<int64_t>(kMaxSlices, std::max<int64_t>(1, (n + slice - 1) / slice)));
+    return static_cast<int>(
+        std::min<int64_t>(kMaxSlices, std::max<int64_t>(1, (n + slice - 1) / slice)));
   };
   p.split_s = cut(max_s);
   p.split_w = cut(max_w);
@@ -1329,6 +1450,25 @@ double visible_pairs(const WindowAttn& w) {
   n += (m * (m + 1) - p0 * (p0 + 1)) / 2;
   n += (p1 - m) * double(std::min(w.window + w.sinks, w.sk));
   return n * double(w.b) * w.heads;
+}
+
+// A launch that may be scheduled while the kernel before it in the stream
+// finishes; the kernel itself waits for that one (pdl_wait) before it touches
+// global memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int block, int smem, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <typename K>
@@ -1406,7 +1546,9 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
     return s;
   const int64_t rows = w.b * w.sq;
   const int64_t pad = w.b * w.heads * (a.sp - w.sq) + 64;
-  const int64_t dsum_blocks = rows + (pad + 255) / 256;
+  const int64_t pairs = rows * w.heads, per_block = 2 * 256 / (DH / 8);
+  const int64_t dsum_rows = (pairs + per_block - 1) / per_block;
+  const int64_t dsum_blocks = dsum_rows + (pad + 255) / 256;
   const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
   dim3 gq(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
   const unsigned gk = static_cast<unsigned>(std::min<int64_t>(p.items, sm_count()));
@@ -1414,17 +1556,23 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
   LaunchScope scope(TP_KIND_ATTN_BWD, 10.0 * DH * visible_pairs(w),
                     double(w.b) * (8.0 * w.sq * nq + 8.0 * w.sk * nk), stream, 3 + joins);
   window_dsum<BF, DH><<<static_cast<unsigned>(dsum_blocks), 256, 0, stream>>>(
-      w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, static_cast<int>(rows), a.sq, a.heads, a.sp);
-  window_bwd_dq<BF, DH><<<gq, kThreads, smem_q, stream>>>(q128, do128, k64, v64, a);
-  window_bwd_dkdv<BF, DH><<<gk, kThreads, smem_kv, stream>>>(k128, v128, q64, do64, a);
-  if (p.split_s > 1)
-    window_kv_join<BF, DH><<<dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0, stream>>>(
-        a, 0, p.split_s, 0);
-  if (p.split_w > 1 && p.key_tiles > p.sink_tiles)
-    window_kv_join<BF, DH><<<dim3((p.key_tiles - p.sink_tiles) * a.bkv, DH / 8, 2), 128, 0,
-                             stream>>>(a, p.sink_tiles, p.split_w,
-                                       p.split_s > 1 ? p.sink_tiles * a.bkv * p.split_s : 0);
+      w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, static_cast<unsigned>(pairs),
+      static_cast<unsigned>(dsum_rows), static_cast<unsigned>(w.b * w.heads), a.sq,
+      static_cast<unsigned>(a.heads), a.sp);
   cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = launch_after(window_bwd_dq<BF, DH>, gq, kThreads, smem_q, stream, q128, do128, k64, v64, a);
+  if (e == cudaSuccess)
+    e = launch_after(window_bwd_dkdv<BF, DH>, dim3(gk), kThreads, smem_kv, stream, k128, v128, q64,
+                     do64, a);
+  if (e == cudaSuccess && p.split_s > 1)
+    e = launch_after(window_kv_join<BF, DH>, dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0, stream,
+                     a, 0, p.split_s, 0);
+  if (e == cudaSuccess && p.split_w > 1 && p.key_tiles > p.sink_tiles)
+    e = launch_after(window_kv_join<BF, DH>,
+                     dim3((p.key_tiles - p.sink_tiles) * a.bkv, DH / 8, 2), 128, 0, stream, a,
+                     p.sink_tiles, p.split_w,
+                     p.split_s > 1 ? p.sink_tiles * a.bkv * p.split_s : 0);
   return e == cudaSuccess ? TP_OK : cuda_fail(e, "window attention backward launch");
 }
 
@@ -1436,7 +1584,7 @@ tp_status window_attn_check(const WindowAttn& w) {
   const int64_t tiles = (w.sk + kBN - 1) / kBN;
   if (tiles * w.b * w.kv_heads > 0x7fffffffLL / kMaxSlices ||
       (w.sq + kB64 - 1) / kB64 * (w.heads / w.kv_heads) > 0x7fffffffLL ||
-      w.b * w.sq > 0x60000000LL || w.b * w.heads > 0x10000000LL)
+      w.b * w.sq * w.heads > 0xe0000000LL || w.b * w.heads > 0x10000000LL)
     return fail(TP_ERR_SHAPE, "window attention: too many key tiles");
   return TP_OK;
 }
