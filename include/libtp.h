@@ -410,8 +410,10 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  * projections, the activation and the product are one kernel, and the shards'
  * products with Wd are summed in its accumulator.
  *   X [M, h]; bgu [2f] = [bg | bu] or NULL; Wd [f, h]; bd [h] or NULL;
- *   Z [M, h]; GUsave [M, 2f] = [G | U] (rounded to bf16) or NULL: kept for
- *   the backward.  H is rounded to bf16 and lives in the workspace.
+ *   Z [M, h]; GUsave [M, 2f] fp16 = [G | U] or NULL: kept for the backward
+ *   (fp16 keeps three more mantissa bits than bf16; a value beyond its range
+ *   is saturated there and reported by tp_device_status() as TP_ERR_KERNEL,
+ *   Z is not affected).  H is rounded to bf16 and lives in the workspace.
  *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
  *   larger batches'.
@@ -429,8 +431,9 @@ tp_status tp_glu_fwd(const void* X, const void* Wgu, const void* bgu, const void
  *   dWd = H^T dZ;  dWgu = X^T [dG | dU];  dX = [dG | dU] Wgu^T (the shards'
  *   and both halves' partials summed in the accumulator);
  *   dbgu = colsum([dG | dU]);  dbd = colsum(dZ).
- *   GUsave: from the forward, or NULL to recompute it from X, Wgu, bgu.
- *   Outputs dX [M, h], dWgu [h, 2f], dWd [f, h], and dbgu [2f], dbd [h] when
+ *   GUsave (fp16): from the forward, or NULL to recompute it from X, Wgu, bgu.
+ *   [dG | dU] and H are rounded to bf16 for the products.  Outputs dX [M, h],
+ *   dWgu [h, 2f], dWd [f, h], and dbgu [2f], dbd [h] when
  *   not NULL; all bf16.  Deterministic.
  * Errors: as tp_glu_fwd; NULL dZ / dX / dWgu / dWd.
  */

@@ -471,14 +471,15 @@ def _glu_sizes(X, Wgu, Wd):
 
 def tp_glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, t: int, act: int, ws, stream=None) -> None:
     """Z = (act(X Wg + bg) * (X Wu + bu)) Wd + bd with Wgu = [Wg | Wu] [h, 2 f];
-    GUsave [M, 2 f] (or None) keeps [G | U] for the backward."""
+    GUsave fp16 [M, 2 f] (or None) keeps [G | U] for the backward."""
     dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
     if _elsewhere(dev, tp_glu_fwd, X, Wgu, bgu, Wd, bd, Z, GUsave, t, act, ws, stream):
         return
     w, wb = _ws(ws, dev)
     status = load().tp_glu_fwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
                                _flat(bd, "bd", h, dt, dev), _flat(Z, "Z", M * h, dt, dev),
-                               _flat(GUsave, "GUsave", 2 * M * f, dt, dev), M, h, f, t, act,
+                               _flat(GUsave, "GUsave", 2 * M * f, torch.float16, dev), M, h, f, t,
+                               act,
                                _dtype(X), w, wb, _raw_stream(stream, dev))
     if status:
         _check(status)
@@ -493,7 +494,7 @@ def tp_glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t: int, ac
         return
     w, wb = _ws(ws, dev)
     status = load().tp_glu_bwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
-                               _flat(GUsave, "GUsave", 2 * M * f, dt, dev),
+                               _flat(GUsave, "GUsave", 2 * M * f, torch.float16, dev),
                                _flat(dZ, "dZ", M * h, dt, dev), _flat(dX, "dX", M * h, dt, dev),
                                _flat(dWgu, "dWgu", 2 * h * f, dt, dev),
                                _flat(dbgu, "dbgu", 2 * f, dt, dev),

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "../../include/libtp.h"
@@ -163,6 +164,39 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
     w[i] = *reinterpret_cast<uint32_t*>(&t);
   }
   return u;
+}
+
+constexpr float kF16Max = 65504.0f;
+
+// Eight fp32 values to fp16, saturated to the finite range; returns whether
+// any finite value had to be clamped.
+__device__ __forceinline__ uint4 pack8_f16(float* f, bool& clamped) {
+  uint4 u;
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (fabsf(f[i]) > kF16Max) {
+      clamped = true;
+      f[i] = copysignf(kF16Max, f[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    __half2 t = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<uint32_t*>(&t);
+  }
+  return u;
+}
+
+// Eight fp16 values as fp32.
+__device__ __forceinline__ void unpack8_f16(const uint4& u, float* f) {
+  const __half2* p = reinterpret_cast<const __half2*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __half22float2(p[i]);
+    f[2 * i] = t.x;
+    f[2 * i + 1] = t.y;
+  }
 }
 
 }  // namespace tp

@@ -916,7 +916,7 @@ tp_status glu_check(int64_t M, int64_t h, int64_t f, int t, tp_act act, tp_dtype
   return check_rows({h, f});
 }
 
-// H = act(X Wg + bg) * (X Wu + bu), [G | U] to GU unless nullptr.
+// H = act(X Wg + bg) * (X Wu + bu), [G | U] (fp16) to GU unless nullptr.
 tp_status glu_up(const void* X, const void* Wgu, const void* bgu, void* H, void* GU, int64_t M,
                  int64_t h, int64_t f, int t, tp_act act, const Tail& tail, cudaStream_t stream) {
   Gemm g;
@@ -1479,8 +1479,9 @@ tp_status tp_device_status(void* stream) {
     const DeviceStatus zero{};
     e = cudaMemcpy(p, &zero, sizeof(zero), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_fail(e, "clearing the device status");
-    const char* sat = (v.flags & kFlagF16Range) ? "; an fp16 attention intermediate (QKV or dO) "
-                                                  "exceeded the fp16 range and was saturated"
+    const char* sat = (v.flags & kFlagF16Range) ? "; an fp16 intermediate (attention QKV or "
+                                                  "dO, the gated block's saved [G | U]) exceeded "
+                                                  "the fp16 range and was saturated"
                                                 : "";
     char buf[256];
     if (v.code != 0) {

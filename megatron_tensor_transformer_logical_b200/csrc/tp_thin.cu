@@ -27,6 +27,7 @@
 // weights: 32 tokens 82 against 84 us (h = 2048: 31 against 39), 64 tokens 150
 // against 88 (52 against 40), so this path ends at 32.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -46,7 +47,9 @@ constexpr int kMinSteps = 4;  // of a warp
 
 struct ThinArgs {
   const __nv_bfloat16 *x, *w, *bias;
-  __nv_bfloat16 *out, *gu;  // gu: [M, 2 N] or nullptr (up product)
+  __nv_bfloat16* out;
+  __half* gu;   // [M, 2 N] or nullptr (up product)
+  WaitCtl status;
   int M, K, N;              // N: columns of H, or of Z
   long long ldw;
   int act;
@@ -102,6 +105,16 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+// Two values in fp16, saturated to its finite range.
+__device__ __forceinline__ __half2 sat_half2(float2 v, bool& clamped) {
+  if (fabsf(v.x) > kF16Max || fabsf(v.y) > kF16Max) {
+    clamped = true;
+    if (fabsf(v.x) > kF16Max) v.x = copysignf(kF16Max, v.x);
+    if (fabsf(v.y) > kF16Max) v.y = copysignf(kF16Max, v.y);
+  }
+  return __floats2half2_rn(v.x, v.y);
 }
 
 template <int MT, bool GLU>
@@ -264,9 +277,11 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
       u.x += bu.x;
       u.y += bu.y;
       if (a.gu != nullptr) {
-        __nv_bfloat16* p = a.gu + static_cast<long long>(t) * 2 * a.N + col;
-        *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(g.x, g.y);
-        *reinterpret_cast<__nv_bfloat162*>(p + a.N) = __floats2bfloat162_rn(u.x, u.y);
+        __half* p = a.gu + static_cast<long long>(t) * 2 * a.N + col;
+        bool clamped = false;
+        *reinterpret_cast<__half2*>(p) = sat_half2(g, clamped);
+        *reinterpret_cast<__half2*>(p + a.N) = sat_half2(u, clamped);
+        if (clamped) status_flag(a.status, kFlagF16Range);
       }
       const float2 v = gate_act2(g, a.act);
       *reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<long long>(t) * a.N + col) =
@@ -347,7 +362,11 @@ tp_status launch_thin_glu(const ThinGlu& g, cudaStream_t stream) {
   a.w = static_cast<const __nv_bfloat16*>(g.wgu);
   a.bias = static_cast<const __nv_bfloat16*>(g.bgu);
   a.out = static_cast<__nv_bfloat16*>(g.H);
-  a.gu = static_cast<__nv_bfloat16*>(g.gu);
+  a.gu = static_cast<__half*>(g.gu);
+  if (a.gu != nullptr) {
+    a.status = wait_ctl();
+    if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
+  }
   a.K = static_cast<int>(g.h);
   a.N = static_cast<int>(g.f);
   a.ldw = 2 * g.f;

@@ -61,7 +61,7 @@ def forward(p, pos, fr):
     L.tp_window_attn_fwd(Qr, Kr, V, O, LSE, B, H, KV, W, SINK)
     L.tp_linear_row(O, p["Wo"], None, A, 1)
     X1 = X + A
-    GU = new(B * S, 2 * F)
+    GU = torch.empty(B * S, 2 * F, dtype=torch.float16, device="cuda")
     L.tp_glu_fwd(X1, p["Wgu"], None, p["Wd"], None, Z, GU, 1, L.TP_ACT_SILU,
                  L.workspace(L.TP_OP_GLU_FWD, B * S, HID, F, 0, 1, L.TP_BF16))
     return X1 + Z, dict(QKV=QKV, Q=Q, K=K, V=V, Qr=Qr, Kr=Kr, O=O, LSE=LSE, X1=X1, GU=GU)
