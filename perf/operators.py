@@ -229,7 +229,7 @@ def _prepare_own(s):
         s["act"] = L.TP_ACT_SILU if case["act"] == "silu" else L.TP_ACT_GELU
         s["ws"] = L.workspace(L.TP_OP_GLU_FWD, M, h, f, 0, t, L.TP_BF16)
         if case["train"]:
-            s["GU"] = torch.empty(M, 2 * f, dtype=torch.bfloat16, device="cuda")
+            s["GU"] = torch.empty(M, 2 * f, dtype=torch.float16, device="cuda")
             s["dX"], s["dWgu"] = torch.empty_like(s["X"]), torch.empty_like(s["Wgu"])
             s["dWd"] = torch.empty_like(s["Wd"])
             s["dbgu"] = torch.empty_like(s["bgu"]) if case["bias"] else None
