@@ -121,6 +121,7 @@ struct WinArgs {
   // dK / dV items: nsink_tiles key tiles hold sinks; the two classes of tiles
   // are cut into split_s and split_w slices; partials of cut tiles in part.
   int bkv, key_tiles, sink_tiles, split_s, split_w, items;
+  int kv_ctas;  // persistent CTAs of the dK / dV part
   float* part;
   WaitCtl status;
 };
@@ -618,13 +619,13 @@ struct DqSmem {
   static constexpr int kBytes = 1024 + 4 * kTile + kKvStages * 2 * kTile64 + 256;
 };
 
-// dQ: one CTA per (sequence, head, pair of query tiles), 64-key blocks.  Per
-// block and tile: S = Q K^T, dP = dO V^T -> dS over S -> dQ += dS K.
+// dQ: one CTA per (sequence, head, pair of query tiles), 64-key blocks; `cta`
+// counts them, heads fastest, longest rows first.  Per block and tile: S = Q
+// K^T, dP = dO V^T -> dS over S -> dQ += dS K.
 template <bool BF, int DH>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                  const WinArgs a) {
+__device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmdO,
+                                       const CUtensorMap& tmK, const CUtensorMap& tmV, int cta,
+                                       const WinArgs& a) {
   constexpr int kTile = DqSmem<DH>::kTile, kTile64 = DqSmem<DH>::kTile64;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -643,8 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int npairs = ((a.sq + kBM - 1) / kBM + 1) / 2;
-  const int pair = npairs - 1 - static_cast<int>(blockIdx.y);
-  const int head = blockIdx.x % a.heads, bi = blockIdx.x / a.heads;
+  const int bh = a.bkv * a.group;
+  const int pair = npairs - 1 - cta / bh;
+  const int head = cta % bh % a.heads, bi = cta % bh / a.heads;
   const int kvh = head / a.group;
   const int r0 = 2 * pair * kBM;
   const BlockList<kB64> bl(r0, a);
@@ -806,9 +808,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
-              const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
-                                           (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
-              const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              g = make_float2((vis >> i) & 1u ? g.x : 0.0f, (vis >> (i + 1)) & 1u ? g.y : 0.0f);
               split2<BF>(g, pk[i >> 1], lk[i >> 1]);
             }
             tmem_st16(tP(x) + lane_off + c / 2, lk);
@@ -824,9 +826,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
-              const float2 e = make_float2((vis >> i) & 1u ? ex2_approx(t.x) : 0.0f,
-                                           (vis >> (i + 1)) & 1u ? ex2_approx(t.y) : 0.0f);
-              const float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              float2 g = __fmul2_rn(e, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd2));
+              g = make_float2((vis >> i) & 1u ? g.x : 0.0f, (vis >> (i + 1)) & 1u ? g.y : 0.0f);
               pk[i >> 1] = pack2<BF>(g.x, g.y);
             }
           }
@@ -948,9 +950,9 @@ __device__ __forceinline__ KvItem kv_item(int k, const WinArgs& a) {
   return it;
 }
 
-// The r-th item of this CTA, or -1: rounds of gridDim.x items in snake order.
+// The r-th item of this CTA, or -1: rounds of kv_ctas items in snake order.
 __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
-  const long long g = gridDim.x, c = blockIdx.x;
+  const long long g = a.kv_ctas, c = blockIdx.x;
   const long long k = r * g + ((r & 1) ? g - 1 - c : c);
   return k < a.items ? static_cast<int>(k) : -1;
 }
@@ -962,12 +964,9 @@ __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
 // products wait until the previous epilogue has read the accumulators
 // (acc_empty).  Items without queries only write zeros.
 template <bool BF, int DH>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_bwd_dkdv(const __grid_constant__ CUtensorMap tmK,
-                    const __grid_constant__ CUtensorMap tmV,
-                    const __grid_constant__ CUtensorMap tmQ,
-                    const __grid_constant__ CUtensorMap tmdO,
-                    const WinArgs a) {
+__device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorMap& tmV,
+                                         const CUtensorMap& tmQ, const CUtensorMap& tmdO,
+                                         const WinArgs& a) {
   constexpr int kTile = KvSmem<DH>::kTile, kTile64 = KvSmem<DH>::kTile64;
   constexpr int kEwWarps = 8;
   extern __shared__ uint8_t smem_raw[];
@@ -1306,6 +1305,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+// Both in one launch: the persistent dK / dV CTAs first, then the dQ CTAs,
+// which fill the SMs that the static split of the key tiles leaves idle at its
+// end (and, on small problems, run beside them).
+template <bool BF, int DH>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd(const __grid_constant__ CUtensorMap q128, const __grid_constant__ CUtensorMap do128,
+               const __grid_constant__ CUtensorMap k64, const __grid_constant__ CUtensorMap v64,
+               const __grid_constant__ CUtensorMap k128, const __grid_constant__ CUtensorMap v128,
+               const __grid_constant__ CUtensorMap q64, const __grid_constant__ CUtensorMap do64,
+               const WinArgs a) {
+  if (static_cast<int>(blockIdx.x) < a.kv_ctas)
+    bwd_dkdv<BF, DH>(k128, v128, q64, do64, a);
+  else
+    bwd_dq<BF, DH>(q128, do128, k64, v64, static_cast<int>(blockIdx.x) - a.kv_ctas, a);
+}
+
 // Adds the slices of one cut key tile in slice order and writes dK (scaled)
 // and dV.  Block (tile slot group, 8 columns, dK or dV): thread = key row.
 template <bool BF, int DH>
@@ -1378,10 +1393,10 @@ bool make_map3(CUtensorMap* m, const void* ptr, bool bf, int64_t cols, int64_t r
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How the key tiles of the dK / dV kernel are cut.  A slice takes at least
-// kMinSlice blocks (about 1.1 us each; its partials cost 128 KB of traffic)
-// and about half of an SM's share of all blocks, so the items balance.
-constexpr int kMinSlice = 16;
+// How the key tiles of the dK / dV kernel are cut.  A slice takes about half
+// of an SM's share of all blocks, so the items balance, but at least 16 blocks
+// (about 1.1 us each; its partials cost 128 KB of traffic), or, where that
+// leaves SMs without an item, an SM's share, at least 4.
 constexpr int kMaxSlices = 255;
 
 struct KvPlan {
@@ -1402,8 +1417,9 @@ KvPlan plan_kv(const WindowAttn& w) {
     int64_t& mx = kb < p.sink_tiles ? max_s : max_w;
     mx = std::max(mx, n);
   }
-  const int64_t share = blocks * bkv / (2 * sm_count());
-  const int64_t slice = std::max<int64_t>(kMinSlice, share);
+  const int64_t share = blocks * bkv / sm_count();
+  const int64_t slice =
+      std::max<int64_t>({4, std::min<int64_t>(16, share), share / 2});
   auto cut = [&](int64_t n) {
     return static_cast<int>(
         std::min<int64_t>(kMaxSlices, std::max<int64_t>(1, (n + slice - 1) / slice)));
@@ -1539,10 +1555,8 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
   a.split_s = p.split_s;
   a.split_w = p.split_w;
   a.items = static_cast<int>(p.items);
-  constexpr int smem_q = DqSmem<DH>::kBytes, smem_kv = KvSmem<DH>::kBytes;
-  if (tp_status s = smem_opt_in(window_bwd_dq<BF, DH>, smem_q, "window dQ smem"); s != TP_OK)
-    return s;
-  if (tp_status s = smem_opt_in(window_bwd_dkdv<BF, DH>, smem_kv, "window dK/dV smem"); s != TP_OK)
+  constexpr int smem = std::max(DqSmem<DH>::kBytes, KvSmem<DH>::kBytes);
+  if (tp_status s = smem_opt_in(window_bwd<BF, DH>, smem, "window backward smem"); s != TP_OK)
     return s;
   const int64_t rows = w.b * w.sq;
   const int64_t pad = w.b * w.heads * (a.sp - w.sq) + 64;
@@ -1550,21 +1564,19 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
   const int64_t dsum_rows = (pairs + per_block - 1) / per_block;
   const int64_t dsum_blocks = dsum_rows + (pad + 255) / 256;
   const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
-  dim3 gq(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
-  const unsigned gk = static_cast<unsigned>(std::min<int64_t>(p.items, sm_count()));
+  a.kv_ctas = static_cast<int>(std::min<int64_t>(p.items, sm_count()));
+  const unsigned grid = static_cast<unsigned>(w.b * w.heads * npairs + a.kv_ctas);
   const int joins = (p.split_s > 1) + (p.split_w > 1 && p.key_tiles > p.sink_tiles);
   LaunchScope scope(TP_KIND_ATTN_BWD, 10.0 * DH * visible_pairs(w),
-                    double(w.b) * (8.0 * w.sq * nq + 8.0 * w.sk * nk), stream, 3 + joins);
+                    double(w.b) * (8.0 * w.sq * nq + 8.0 * w.sk * nk), stream, 2 + joins);
   window_dsum<BF, DH><<<static_cast<unsigned>(dsum_blocks), 256, 0, stream>>>(
       w.o, w.ldo, w.d_o, w.lddo, w.lse, nlse, nd, static_cast<unsigned>(pairs),
       static_cast<unsigned>(dsum_rows), static_cast<unsigned>(w.b * w.heads), a.sq,
       static_cast<unsigned>(a.heads), a.sp);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_after(window_bwd_dq<BF, DH>, gq, kThreads, smem_q, stream, q128, do128, k64, v64, a);
-  if (e == cudaSuccess)
-    e = launch_after(window_bwd_dkdv<BF, DH>, dim3(gk), kThreads, smem_kv, stream, k128, v128, q64,
-                     do64, a);
+    e = launch_after(window_bwd<BF, DH>, dim3(grid), kThreads, smem, stream, q128, do128, k64, v64,
+                     k128, v128, q64, do64, a);
   if (e == cudaSuccess && p.split_s > 1)
     e = launch_after(window_kv_join<BF, DH>, dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0, stream,
                      a, 0, p.split_s, 0);
@@ -1579,12 +1591,13 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
 }  // namespace
 
 tp_status window_attn_check(const WindowAttn& w) {
-  if ((w.sq + kBM - 1) / kBM > 65535 || w.b * w.heads > 0x7fffffffLL)
+  const int64_t q_tiles = (w.sq + kBM - 1) / kBM;
+  if (q_tiles > 65535 || w.b * w.heads > 0x10000000LL || w.b * w.heads * q_tiles > 0x70000000LL)
     return fail(TP_ERR_SHAPE, "window attention: sequence or b * heads too large");
   const int64_t tiles = (w.sk + kBN - 1) / kBN;
   if (tiles * w.b * w.kv_heads > 0x7fffffffLL / kMaxSlices ||
       (w.sq + kB64 - 1) / kB64 * (w.heads / w.kv_heads) > 0x7fffffffLL ||
-      w.b * w.sq * w.heads > 0xe0000000LL || w.b * w.heads > 0x10000000LL)
+      w.b * w.sq * w.heads > 0xe0000000LL)
     return fail(TP_ERR_SHAPE, "window attention: too many key tiles");
   return TP_OK;
 }
