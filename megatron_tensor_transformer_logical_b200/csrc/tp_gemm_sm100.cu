@@ -304,12 +304,13 @@ __device__ __forceinline__ float warp_colsum32(float (&v)[32], int lane) {
 // The bias gradient of a GeLU' epilogue: after the epilogue has left the
 // output values of rows row0 + lane (row0 a multiple of 32) and columns
 // [col0, col0 + 32) in v, adds this warp's 32-row column sums to the
-// partial array (rows past M and columns past col_end count as zero).
+// partial array (rows past M and columns past col_end count as zero; a warp
+// whose rows all lie past M has no row in the array).
 template <int EPI>
 __device__ __forceinline__ void epilogue_colsum(float (&v)[32], int row, int col0, int col_end,
                                                 int lane, const Args& a) {
   if constexpr (EPI == kEpiDGelu) {
-    if (a.csum_part == nullptr) return;
+    if (a.csum_part == nullptr || (row & ~31) >= a.M) return;
     if (row >= a.M) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] = 0.0f;
@@ -322,6 +323,7 @@ __device__ __forceinline__ void epilogue_colsum(float (&v)[32], int row, int col
 
 // Adds a warp's 32-row column sums of one half of a gated gradient to the
 // partials (rows past M and columns past col_end count as zero).  Destroys v.
+// The warp's first row lies before M.
 __device__ __forceinline__ void glu_colsum(float (&v)[32], int row, int ncols, int pcol0, int lane,
                                            const Args& a) {
   if (row >= a.M) {
@@ -399,7 +401,7 @@ __device__ __forceinline__ void epilogue_dglu_row32(float (&v)[32], float (&du)[
 __device__ __forceinline__ void epilogue_glu_colsum(float (&dg)[32], float (&du)[32], int row,
                                                     int col0, int col_end, int lane,
                                                     const Args& a) {
-  if (a.csum_part == nullptr) return;
+  if (a.csum_part == nullptr || (row & ~31) >= a.M) return;
   glu_colsum(dg, row, col_end - col0, col0, lane, a);
   glu_colsum(du, row, col_end - col0, a.N + col0, lane, a);
 }

@@ -294,6 +294,42 @@ def test_workspace_without_the_optional_part():
     compare({"Z": Z}, ref, tol)
 
 
+@pytest.mark.parametrize("M", [1, 33, 130])
+def test_a_backward_stays_inside_its_workspace(M):
+    """Rows past M have no place in the bias gradients' partial sums: bytes
+    behind the smallest workspace the calls take stay as they were, and other
+    parts of it intact (the results are right)."""
+    h, f = 256, 4096
+    d = make(M, h, f, True, 13)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tail = (4096 + sms * 128 * 256 * 4 + 255) // 256 * 256 + 256  # the optional part
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")
+    GU = torch.empty(M, 2 * f, dtype=torch.float16, device="cuda")
+    L.tp_glu_fwd(d["X"], d["Wgu"], d["bgu"], d["Wd"], d["bd"], e(M, h), GU, 1, 0,
+                 L.workspace(L.TP_OP_GLU_FWD, M, h, f, 0, 1, L.TP_BF16))
+    need = L.tp_workspace_size(L.TP_OP_GLU_BWD, M, h, f, 0, 1, L.TP_BF16) - tail
+    buf = torch.full((need + (8 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    out = dict(dX=e(M, h), dWgu=e(h, 2 * f), dWd=e(f, h), dbgu=e(2 * f), dbd=e(h))
+    L.tp_glu_bwd(d["X"], d["Wgu"], d["bgu"], d["Wd"], GU, d["dZ"], out["dX"], out["dWgu"],
+                 out["dbgu"], out["dWd"], out["dbd"], 1, 0, buf[:need])
+    assert (buf[need:] == 0x5a).all()
+    ref, tol = reference(d, "silu")
+    compare(out, ref, tol)
+    # the same for the plain MLP's backward
+    A, B, Y, bA = d["Wgu"][:, :f].contiguous(), d["Wd"], e(M, f), d["bgu"][:f].contiguous()
+    L.tp_mlp_fwd(d["X"], A, bA, B, d["bd"], e(M, h), Y, 1,
+                 L.workspace(L.TP_OP_MLP_FWD, M, h, f, 0, 1, L.TP_BF16))
+    need = L.tp_workspace_size(L.TP_OP_MLP_BWD, M, h, f, 0, 1, L.TP_BF16) - tail
+    buf = torch.full((need + (8 << 20),), 0x5a, dtype=torch.uint8, device="cuda")
+    dbA = e(f)
+    L.tp_mlp_bwd(d["X"], A, bA, B, Y, d["dZ"], e(M, h), e(h, f), dbA, e(f, h), e(h), 1, buf[:need])
+    assert (buf[need:] == 0x5a).all()
+    Yd = Y.double()
+    cdf = torch.special.ndtr(Yd)
+    dY = (d["dZ"].double() @ B.double().t()) * (cdf + Yd * torch.exp(-Yd * Yd / 2) * 0.3989422804014327)
+    assert ((dbA.double() - dY.sum(0)).norm() / dY.sum(0).norm()).item() <= 5e-3
+
+
 def test_binding_refuses_mismatched_tensors():
     d = make(4, 64, 128, True, 11)
     Z, ws = torch.empty_like(d["X"]), L.workspace(L.TP_OP_GLU_FWD, 4, 64, 128, 0, 1, L.TP_BF16)
