@@ -135,6 +135,13 @@ __device__ __forceinline__ void status_flag(const WaitCtl& w, int bits) {
   atomicOr(&w.st->flags, bits);
 }
 
+// Programmatic launches: lets the next kernel of the stream be scheduled; and
+// waits until the kernels before this one are complete.
+__device__ __forceinline__ void pdl_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ------------------------------------------------------------- arithmetic
 // 2^x by the hardware's approximate base-2 exponential (PTX ex2.approx.ftz:
 // relative error about 2^-22, subnormal results flushed to zero, 2^-inf = 0).

@@ -28,6 +28,25 @@ int sm_count();
 // it cannot be queried.  Caches of device-symbol addresses key on it.
 unsigned long long current_context_id();
 
+// Launches a kernel.  With `after` it may be scheduled while the kernel before
+// it in the stream finishes; it then waits for that one itself (pdl_wait)
+// before it touches global memory.
+template <typename... P, typename... A>
+cudaError_t launch_kernel(void (*kern)(P...), dim3 grid, int block, int smem, cudaStream_t stream,
+                          bool after, const A&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Brackets one kernel launch: counts it and, while profiling is enabled,
 // records a start/stop event pair on `stream` with its kind and work.
 class LaunchScope {

@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i)
     if (i < n) fetch_w(i);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (a.pdl) asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_next();
+  if (a.pdl) pdl_wait();
 #pragma unroll
   for (int i = 0; i < C::kStages - 1; ++i) {
     if (i < n) fetch_x(i);

@@ -270,13 +270,6 @@ __device__ __forceinline__ float exp_row_masked(uint32_t srow, const RowMask& ma
   return acc.x + acc.y;
 }
 
-// Programmatic launches: lets the next kernel of the stream be scheduled; and
-// waits until the kernels before this one are complete.
-__device__ __forceinline__ void pdl_next() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // One box per 64 columns of a [rows x DH] tile; the halves are rows * 128
 // bytes apart.
 template <int DH>
@@ -1468,25 +1461,6 @@ double visible_pairs(const WindowAttn& w) {
   return n * double(w.b) * w.heads;
 }
 
-// A launch that may be scheduled while the kernel before it in the stream
-// finishes; the kernel itself waits for that one (pdl_wait) before it touches
-// global memory.
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kern)(P...), dim3 grid, int block, int smem, cudaStream_t stream,
-                         const A&... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <typename K>
 tp_status smem_opt_in(K kern, int bytes, const char* what) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
@@ -1575,16 +1549,16 @@ tp_status bwd(const WindowAttn& w, void* scratch, cudaStream_t stream) {
       static_cast<unsigned>(a.heads), a.sp);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_after(window_bwd<BF, DH>, dim3(grid), kThreads, smem, stream, q128, do128, k64, v64,
-                     k128, v128, q64, do64, a);
+    e = launch_kernel(window_bwd<BF, DH>, dim3(grid), kThreads, smem, stream, true, q128, do128, k64,
+                      v64, k128, v128, q64, do64, a);
   if (e == cudaSuccess && p.split_s > 1)
-    e = launch_after(window_kv_join<BF, DH>, dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0, stream,
-                     a, 0, p.split_s, 0);
+    e = launch_kernel(window_kv_join<BF, DH>, dim3(p.sink_tiles * a.bkv, DH / 8, 2), 128, 0,
+                      stream, true, a, 0, p.split_s, 0);
   if (e == cudaSuccess && p.split_w > 1 && p.key_tiles > p.sink_tiles)
-    e = launch_after(window_kv_join<BF, DH>,
-                     dim3((p.key_tiles - p.sink_tiles) * a.bkv, DH / 8, 2), 128, 0, stream, a,
-                     p.sink_tiles, p.split_w,
-                     p.split_s > 1 ? p.sink_tiles * a.bkv * p.split_s : 0);
+    e = launch_kernel(window_kv_join<BF, DH>,
+                      dim3((p.key_tiles - p.sink_tiles) * a.bkv, DH / 8, 2), 128, 0, stream, true,
+                      a, p.sink_tiles, p.split_w,
+                      p.split_s > 1 ? p.sink_tiles * a.bkv * p.split_s : 0);
   return e == cudaSuccess ? TP_OK : cuda_fail(e, "window attention backward launch");
 }
 

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
   const int rows = min(a.group - gt * kRows, kRows);
   const int head0 = kvh * a.group + gt * kRows;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may be scheduled
+  pdl_next();  // the join may be scheduled
   const Visible vis(a.lens[bi], a);
   const int per = slice_keys(vis.total, a.splits);
   const int t0 = min(split * per, vis.total), t1 = min(t0 + per, vis.total);
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
   const int item = (bi * a.kv_heads + kvh) * a.gtiles + gh / kRows;
   const long long p0 = static_cast<long long>(item) * a.splits * a.rows + gh % kRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the slices are complete
+  pdl_wait();  // the slices are complete
   // one slice per thread (splits <= 255): the common maximum, then the weights
   const float2 ml = static_cast<int>(threadIdx.x) < a.splits
                         ? a.pml[p0 + static_cast<long long>(threadIdx.x) * a.rows]
@@ -463,16 +463,8 @@ tp_status decode(const WindowDecode& w, void* scratch, cudaStream_t stream) {
   e = cudaGetLastError();
   if (e == cudaSuccess && a.splits > 1) {
     // Scheduled while the slices finish; it waits for them itself.
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(w.b * w.heads));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, window_decode_join<BF, DH>, a);
+    e = launch_kernel(window_decode_join<BF, DH>, dim3(static_cast<unsigned>(w.b * w.heads)), 256, 0,
+                      stream, true, a);
   }
   return e == cudaSuccess ? TP_OK : cuda_fail(e, "window decode launch");
 }
