@@ -148,22 +148,35 @@ __device__ __forceinline__ Blocks blocks_of(int r0, const WinArgs& a) {
   return b;
 }
 
-// The CTA's list of key blocks for its two query tiles: sink blocks [0, ns),
-// then [lo, hi].  Every listed block is seen by one of the tiles at least.
+// The CTA's list of key blocks for its two query tiles: [lo, hi], then sink
+// blocks [0, ns).  Every listed block is seen by one of the tiles at least.
+// With keys in front of the window, [lo, hi] runs from the diagonal down: each
+// row then meets visible keys, itself among them, in its tile's first block,
+// where the first block of the window may hide all of its keys from the last
+// rows and send them through the exact maximum a block later (187 against 194
+// us on 8192 tokens, 32 heads, window 1024, 4 sinks).  Without, it runs up
+// from block 0, where every row sees keys and the two tiles end a block apart,
+// so that one tile's epilogue overlaps the other's last block (68 against 76
+// us on 4096 tokens, 16 heads, all visible).
 template <int BN>
 struct BlockList {
   Blocks t0, t1;
-  int nsb, ns, lo, n;
+  int nsb, ns, lo, hi, n;
+  bool down;
   __device__ __forceinline__ BlockList(int r0, const WinArgs& a) {
     t0 = blocks_of<BN>(r0, a);
     t1 = blocks_of<BN>(r0 + kBM, a);
     nsb = (a.sinks + BN - 1) / BN;
     lo = t0.lo;
-    const int hi = max(t0.hi, t1.hi);
+    hi = max(t0.hi, t1.hi);
+    down = lo > 0;
     ns = hi < 0 ? 0 : min(nsb, lo);
     n = hi < 0 ? 0 : ns + hi - lo + 1;
   }
-  __device__ __forceinline__ int block(int j) const { return j < ns ? j : lo + (j - ns); }
+  __device__ __forceinline__ int block(int j) const {
+    if (j >= n - ns) return j - (n - ns);
+    return down ? hi - j : j;  // lo = 0 when it runs up
+  }
   __device__ __forceinline__ bool sees(int x, int j) const {
     const int kb = block(j);
     const int xlo = x ? t1.lo : t0.lo, xhi = x ? t1.hi : t0.hi;
@@ -202,6 +215,12 @@ struct RowMask {
   }
 };
 
+// Whether all rows of a tile, positions [p0, p0 + 128), see all of the key
+// block at k0.
+__device__ __forceinline__ bool all_visible(int p0, int k0, const WinArgs& a) {
+  return k0 + kBN - 1 <= p0 && (k0 > p0 + kBM - 1 - a.window || k0 + kBN <= a.sinks);
+}
+
 // Row with query position p (p < sk) in the key block that starts at k0.
 __device__ __forceinline__ RowMask row_mask(int p, int k0, const WinArgs& a) {
   RowMask m;
@@ -228,14 +247,20 @@ __device__ __forceinline__ float row_max_masked(uint32_t srow, const RowMask& m)
   return mx;
 }
 
-// P = 2^(s * scale_log2 - m) over one block row (hidden keys 0), packed in
-// registers; returns the row sum of the unrounded P.
-template <bool BF>
-__device__ __forceinline__ float exp_row_masked(uint32_t srow, const RowMask& mask,
-                                                float scale_log2, float m,
-                                                uint32_t (&pk)[kBN / 2]) {
+// P = 2^(s * scale_log2 - m) over one block row, packed in registers; returns
+// the row sum of the unrounded P.  ALL: every row of the tile sees the whole
+// block.  Otherwise hidden keys give 0, and a chunk that no row of the warp
+// sees costs no exponential.  (Leaving the columns behind the sinks out of a
+// sink block's products as well was slower, 196 against 188 us on the case
+// above: the issuing thread's branches cost more than the narrow products
+// save.)
+template <bool BF, bool ALL>
+__device__ __forceinline__ float exp_row(uint32_t srow, const RowMask& mask, float scale_log2,
+                                         float m, uint32_t (&pk)[kBN / 2]) {
   const float2 sc2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m, -m);
   float2 acc = make_float2(0.0f, 0.0f);
+  // The next chunk's tensor-memory load is in flight while this one is
+  // computed (one wait per chunk, after the computation).
   uint32_t nx[32];
   tmem_ld32_nowait(srow, nx);
   tmem_wait_ld(nx);
@@ -245,26 +270,28 @@ __device__ __forceinline__ float exp_row_masked(uint32_t srow, const RowMask& ma
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(nx[i]);
     if (c + 32 < kBN) tmem_ld32_nowait(srow + c + 32, nx);
-    float2 u[16];
+    const uint32_t vis = ALL ? 0xffffffffu : mask.bits(c);
+    if (ALL || __any_sync(0xffffffffu, vis != 0u)) {
+      float2 u[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float2 t = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
-      u[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      for (int i = 0; i < 16; ++i) {
+        const float2 t = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), sc2, nm2);
+        u[i] = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+        if (!ALL)
+          u[i] = make_float2((vis >> (2 * i)) & 1u ? u[i].x : 0.0f,
+                             (vis >> (2 * i + 1)) & 1u ? u[i].y : 0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[c / 2 + i] = pack2<BF>(u[i].x, u[i].y);
+#pragma unroll
+      for (int k = 8; k >= 1; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < k; ++i) u[i] = __fadd2_rn(u[i], u[i + k]);
+      acc = __fadd2_rn(acc, u[0]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[c / 2 + i] = 0u;
     }
-    if (!mask.full(c)) {
-      const uint32_t vis = mask.bits(c);
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        u[i] = make_float2((vis >> (2 * i)) & 1u ? u[i].x : 0.0f,
-                           (vis >> (2 * i + 1)) & 1u ? u[i].y : 0.0f);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) pk[c / 2 + i] = pack2<BF>(u[i].x, u[i].y);
-#pragma unroll
-    for (int k = 8; k >= 1; k >>= 1)
-#pragma unroll
-      for (int i = 0; i < k; ++i) u[i] = __fadd2_rn(u[i], u[i + k]);
-    acc = __fadd2_rn(acc, u[0]);
     if (c + 32 < kBN) tmem_wait_ld(nx);
   }
   return acc.x + acc.y;
@@ -452,13 +479,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                            kStatusAttnTimeout)))
         break;
       tc_fence_after();
-      const RowMask mask = row_mask(p, bl.block(j) * kBN, a);
+      const int k0 = bl.block(j) * kBN;
+      const RowMask mask = row_mask(p, k0, a);
+      const bool all = all_visible(r0 + x * kBM + a.off, k0, a);
       if (cnt == 0) m_used = row_max_masked(srow, mask) * a.scale_log2;
       uint32_t pk[kBN / 2];
       // A row that has seen no key yet (m_used = -inf) has P = 0 by the mask;
       // 0 stands in for its maximum.
-      float rs = exp_row_masked<BF>(srow, mask, a.scale_log2,
-                                    m_used == -INFINITY ? 0.0f : m_used, pk);
+      float rs = all ? exp_row<BF, true>(srow, mask, a.scale_log2,
+                                         m_used == -INFINITY ? 0.0f : m_used, pk)
+                     : exp_row<BF, false>(srow, mask, a.scale_log2,
+                                          m_used == -INFINITY ? 0.0f : m_used, pk);
       // The first block set the maximum in use, so its P <= 1.  Later blocks:
       // a row sum above kCheckSum, or a row without a maximum so far, sends
       // the warp to the exact maximum.
@@ -471,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           // this S) and l.  From -inf the factor is 0, on sums that are 0.
           const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
           if (need) m_used = m_new;
-          rs = exp_row_masked<BF>(srow, mask, a.scale_log2, m_used == -INFINITY ? 0.0f : m_used,
-                                  pk);
+          rs = exp_row<BF, false>(srow, mask, a.scale_log2,
+                                  m_used == -INFINITY ? 0.0f : m_used, pk);
 #pragma unroll 1
           for (int c = 0; c < DH; c += 32) {
             float o[32];
@@ -795,8 +826,13 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
           tmem_ld32x2(tS(x) + lane_off + c, sv, tP(x) + lane_off + c, pv);
           uint32_t pk[16];
           const uint32_t vis = mask.full(c) ? 0xffffffffu : mask.bits(c);
-          // dS = P (dP - D), two entries at a time.
-          if constexpr (two) {
+          // dS = P (dP - D), two entries at a time; no work for a chunk that no
+          // row of the warp sees.
+          if (!__any_sync(0xffffffffu, vis != 0u)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = 0u;
+            if constexpr (two) tmem_st16(tP(x) + lane_off + c / 2, pk);
+          } else if constexpr (two) {
             uint32_t lk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
@@ -1195,7 +1231,14 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
           uint32_t pk[16], dk[16];
           const bool full = lo <= 0 && hi >= 32;
           const uint32_t vis = full ? 0xffffffffu : RowMask::prefix(hi) & ~RowMask::prefix(lo);
-          if constexpr (two) {
+          if (!__any_sync(0xffffffffu, vis != 0u)) {  // no key of this warp sees a query
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = dk[i] = 0u;
+            if constexpr (two) {
+              tmem_st16(tS(st) + lane_off + c + 16, pk);
+              tmem_st16(tP(st) + lane_off + c + 16, dk);
+            }
+          } else if constexpr (two) {
             uint32_t pl[16], dl[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
