@@ -369,19 +369,22 @@ def _device_of(t) -> int:
     return dev
 
 
-def _elsewhere(dev: int, fn, *args) -> bool:
-    """Calls fn(*args) with device `dev` current, if it is not already."""
-    if torch._C._cuda_getDevice() == dev:
-        return False
+# The current device, and the raw handle of a device's current stream.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _elsewhere(dev: int, fn, *args) -> None:
+    """fn(*args) with device `dev` current."""
     with torch.cuda.device(dev):
         fn(*args)
-    return True
 
 
 def _raw_stream(stream, dev: int):
     """The given stream's handle, else that of the device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
+        return _current_raw_stream(dev)
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -410,9 +413,9 @@ def tp_qk_norm_rope_fwd(Q, K, gq, gk, pos, inv_freq, Qo, Ko, d: int, norm: bool 
     [M, kv_heads * d] (row-strided views allowed, K may be None), pos int32 [M],
     inv_freq fp64 [d_rot / 2] (None: no rotation).  Qo may be Q, Ko may be K."""
     dev = _device_of(Q)
-    if _elsewhere(dev, tp_qk_norm_rope_fwd, Q, K, gq, gk, pos, inv_freq, Qo, Ko, d, norm,
-                  interleaved, eps, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_qk_norm_rope_fwd, Q, K, gq, gk, pos, inv_freq, Qo, Ko, d, norm,
+                          interleaved, eps, stream)
     sq, sk, dt, M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq,
                                                                      d, dev)
     q, ldq = _rows(Q, "Q", sq, dt, dev)
@@ -432,9 +435,9 @@ def tp_qk_norm_rope_bwd(Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq, dgk,
     """Backward of tp_qk_norm_rope_fwd from its inputs Q, K and the gradients dQo,
     dKo of its outputs; dQ may be dQo, dK may be dKo; dgq, dgk may be None."""
     dev = _device_of(Q)
-    if _elsewhere(dev, tp_qk_norm_rope_bwd, Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK, dgq,
-                  dgk, d, ws, norm, interleaved, eps, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_qk_norm_rope_bwd, Q, K, gq, gk, pos, inv_freq, dQo, dKo, dQ, dK,
+                          dgq, dgk, d, ws, norm, interleaved, eps, stream)
     sq, sk, dt, M, heads, kv, d_rot, pgq, pgk, ppos, pfr = _qk_sizes(Q, K, gq, gk, pos, inv_freq,
                                                                      d, dev)
     q, ldq = _rows(Q, "Q", sq, dt, dev)
@@ -473,8 +476,8 @@ def tp_glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, t: int, act: int, ws, stream=None
     """Z = (act(X Wg + bg) * (X Wu + bu)) Wd + bd with Wgu = [Wg | Wu] [h, 2 f];
     GUsave fp16 [M, 2 f] (or None) keeps [G | U] for the backward."""
     dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
-    if _elsewhere(dev, tp_glu_fwd, X, Wgu, bgu, Wd, bd, Z, GUsave, t, act, ws, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_glu_fwd, X, Wgu, bgu, Wd, bd, Z, GUsave, t, act, ws, stream)
     w, wb = _ws(ws, dev)
     status = load().tp_glu_fwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
                                _flat(bd, "bd", h, dt, dev), _flat(Z, "Z", M * h, dt, dev),
@@ -489,9 +492,9 @@ def tp_glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t: int, ac
                stream=None) -> None:
     """Backward of tp_glu_fwd; GUsave None recomputes [G | U]; dbgu, dbd may be None."""
     dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
-    if _elsewhere(dev, tp_glu_bwd, X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t, act,
-                  ws, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_glu_bwd, X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t,
+                          act, ws, stream)
     w, wb = _ws(ws, dev)
     status = load().tp_glu_bwd(x, wgu, _flat(bgu, "bgu", 2 * f, dt, dev), wd,
                                _flat(GUsave, "GUsave", 2 * M * f, torch.float16, dev),
@@ -523,9 +526,9 @@ def tp_window_attn_fwd(Q, K, V, O, LSE, b: int, heads: int, kv_heads: int, windo
     before it and the first `sinks` keys.  LSE fp32 [b, heads, sq]; scale 0: 1 /
     sqrt(d)."""
     dev = _device_of(Q)
-    if _elsewhere(dev, tp_window_attn_fwd, Q, K, V, O, LSE, b, heads, kv_heads, window, sinks,
-                  scale, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_window_attn_fwd, Q, K, V, O, LSE, b, heads, kv_heads, window,
+                          sinks, scale, stream)
     shq, shk, dt, sq, sk, d = _window_sizes(Q, K, b, heads, kv_heads)
     q, ldq = _rows(Q, "Q", shq, dt, dev)
     k, ldk = _rows(K, "K", shk, dt, dev)
@@ -543,9 +546,9 @@ def tp_window_attn_bwd(Q, K, V, O, LSE, dO, dQ, dK, dV, b: int, heads: int, kv_h
                        window: int, sinks: int, ws, scale: float = 0.0, stream=None) -> None:
     """Backward of tp_window_attn_fwd; ws from window_attn_workspace()."""
     dev = _device_of(Q)
-    if _elsewhere(dev, tp_window_attn_bwd, Q, K, V, O, LSE, dO, dQ, dK, dV, b, heads, kv_heads,
-                  window, sinks, ws, scale, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_window_attn_bwd, Q, K, V, O, LSE, dO, dQ, dK, dV, b, heads,
+                          kv_heads, window, sinks, ws, scale, stream)
     shq, shk, dt, sq, sk, d = _window_sizes(Q, K, b, heads, kv_heads)
     args = []
     for t, n, sh in ((Q, "Q", shq), (K, "K", shk), (V, "V", shk), (O, "O", shq)):
@@ -566,9 +569,9 @@ def tp_window_attn_decode(Q, K, V, lens, O, LSE, heads: int, kv_heads: int, wind
     kv_heads * d] (strided views allowed), lens int32 [b] on the device (keys per
     sequence, the new token's included), LSE fp32 [b, heads] or None."""
     dev = _device_of(Q)
-    if _elsewhere(dev, tp_window_attn_decode, Q, K, V, lens, O, LSE, heads, kv_heads, window,
-                  sinks, ws, scale, stream):
-        return
+    if _current_device() != dev:
+        return _elsewhere(dev, tp_window_attn_decode, Q, K, V, lens, O, LSE, heads, kv_heads,
+                          window, sinks, ws, scale, stream)
     shq, shk, dt = Q.shape, K.shape, Q.dtype
     if dt not in _HALF:
         raise ValueError(f"unsupported dtype {dt}")
