@@ -413,7 +413,8 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  *   Z [M, h]; GUsave [M, 2f] fp16 = [G | U] or NULL: kept for the backward
  *   (fp16 keeps three more mantissa bits than bf16; a value beyond its range
  *   is saturated there and reported by tp_device_status() as TP_ERR_KERNEL,
- *   Z is not affected).  H is rounded to bf16 and lives in the workspace.
+ *   Z is not affected).  H lives in the workspace, rounded to bf16 (up to 8
+ *   tokens with the rounded rest as a second term).
  *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
  *   larger batches'.

@@ -893,7 +893,10 @@ tp_status vocab_ce_bwd(const void* X, const void* E, const int32_t* targets, con
 
 // ------------------------------------------------ gated feed-forward block
 
-size_t glu_fwd_ws_min(int64_t M, int64_t f) { return align_up(M * f * 2, 256) + 256; }
+// H, in two terms for the fewest tokens.
+size_t glu_h_bytes(int64_t M, int64_t f) { return M * f * 2 * (M <= kThinTwoTermM ? 2 : 1); }
+
+size_t glu_fwd_ws_min(int64_t M, int64_t f) { return align_up(glu_h_bytes(M, f), 256) + 256; }
 
 size_t glu_bwd_colsum_bytes(int64_t M, int64_t h, int64_t f) {
   return align_up(dba_partial_bytes(M, 2 * f), 256) + mlp_bias_grads_scratch_bytes(M, h);
@@ -942,7 +945,7 @@ tp_status glu_fwd(const void* X, const void* Wgu, const void* bgu, const void* W
   if (ws == nullptr || ws_bytes < glu_fwd_ws_min(M, f))
     return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_workspace_size()");
   Carve c(ws, ws_bytes);
-  void* H = c.take(M * f * 2);
+  void* H = c.take(glu_h_bytes(M, f));
   if (M <= kThinMaxM) {
     ThinGlu g;
     g.x = X; g.wgu = Wgu; g.bgu = bgu; g.wd = Wd; g.bd = bd;

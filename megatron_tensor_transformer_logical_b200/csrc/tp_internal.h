@@ -143,8 +143,9 @@ struct Gemm {
 
 // The gated block's forward on a few tokens (M <= kThinMaxM), by kernels that
 // stream the weights: H = act(x wgu + bgu) ([g | u] to gu unless nullptr), z =
-// H wd + bd.
-constexpr int64_t kThinMaxM = 32;
+// H wd + bd.  H is bf16 [M, f], the rounded values; up to kThinTwoTermM tokens
+// a second matrix, of the rests, follows.
+constexpr int64_t kThinMaxM = 32, kThinTwoTermM = 8;
 struct ThinGlu {
   const void *x = nullptr, *wgu = nullptr, *bgu = nullptr, *wd = nullptr, *bd = nullptr;
   void *H = nullptr, *gu = nullptr, *z = nullptr;

@@ -14,11 +14,16 @@
 //   (a cluster of blocks) through distributed shared memory, in a fixed
 //   order; then bias, activation and product.  Nothing goes through HBM but
 //   the weights, X, H and Z.
+// * Up to 8 tokens H goes from one product to the other as two bf16 terms, the
+//   rounded value and the rounded rest (60.4 against 59.2 us for one token):
+//   few outputs do not average, and Z is then off by its own rounding alone,
+//   not by 1.4 times that.  At 13 tokens the second term would cost 6% (25.1
+//   against 23.6 us), at 32 tokens 12%.
 // * The down product is launched with programmatic stream serialisation: its
 //   blocks start as the up product's finish, request their first weight tiles,
 //   and only then wait for H.
 // All blocks run at once, two per SM (clusters are sized for that).
-// Measured: one token, h = 4096, f = 14336 (352 MB of weights) 59 us, 6.0 TB/s
+// Measured: one token, h = 4096, f = 14336 (352 MB of weights) 60 us, 5.8 TB/s
 // over both products; 13 tokens, h = 2048, f = 5632 (69 MB) 23.6 us.  Tried on
 // these: five stages 61 / 23.7 us, three 62 / 24.1; clusters up to 16 blocks
 // 72 / 27; blocks of 4 warps, five per SM, 81 / 29; an even share of all slabs
@@ -47,7 +52,7 @@ constexpr int kMinSteps = 4;  // of a warp
 
 struct ThinArgs {
   const __nv_bfloat16 *x, *w, *bias;
-  __nv_bfloat16* out;
+  __nv_bfloat16* out;       // up: the terms of H, [terms][M, N]
   __half* gu;   // [M, 2 N] or nullptr (up product)
   WaitCtl status;
   int M, K, N;              // N: columns of H, or of Z
@@ -57,11 +62,12 @@ struct ThinArgs {
   int pdl;      // wait for the previous kernel before reading x
 };
 
-template <int MT>
+template <int MT, int TERMS>
 struct Cfg {
   static constexpr int kStages = 4;
   static constexpr int kWBytes = kStepK * kCols * 2;         // 2 KB
-  static constexpr int kXBytes = MT * 16 * kStepK * 2;       // 512 bytes per 16 tokens
+  static constexpr int kXTerm = MT * 16 * kStepK * 2;        // 512 bytes per 16 tokens
+  static constexpr int kXBytes = TERMS * kXTerm;
   static constexpr int kStageBytes = kWBytes + kXBytes;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kRed = kWarps * 16 * kCols * 4;       // one m-tile of every warp
@@ -91,7 +97,7 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -117,9 +123,9 @@ __device__ __forceinline__ __half2 sat_half2(float2 v, bool& clamped) {
   return __floats2half2_rn(v.x, v.y);
 }
 
-template <int MT, bool GLU>
+template <int MT, bool GLU, int TERMS>
 __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
-  using C = Cfg<MT>;
+  using C = Cfg<MT, TERMS>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = a.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -159,8 +165,10 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
     for (int mt = 0; mt < MT; ++mt) {
       const int t = 16 * mt + (lane >> 1);
       const bool ok = t < a.M && k < a.K;
-      cp_async16(st + t * 32 + (((lane & 1) ^ ((t >> 2) & 1)) << 4),
-                 ok ? a.x + static_cast<long long>(t) * a.K + k : a.x, ok);
+#pragma unroll
+      for (int e = 0; e < TERMS; ++e)
+        cp_async16(st + e * C::kXTerm + t * 32 + (((lane & 1) ^ ((t >> 2) & 1)) << 4),
+                   ok ? a.x + (static_cast<long long>(e) * a.M + t) * a.K + k : a.x, ok);
     }
   };
 
@@ -195,21 +203,25 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     const uint32_t sw = ring + (i % C::kStages) * C::kStageBytes, sx = sw + C::kWBytes;
-    uint32_t xf[MT][4];
+    uint32_t xf[TERMS][MT][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int t = 16 * mt + xrow;
-      ldmatrix4<false>(xf[mt], sx + t * 32 + ((xhalf ^ ((t >> 2) & 1)) << 4));
-    }
+    for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int t = 16 * mt + xrow;
+        ldmatrix4<false>(xf[e][mt], sx + e * C::kXTerm + t * 32 + ((xhalf ^ ((t >> 2) & 1)) << 4));
+      }
 #pragma unroll
     for (int c = 0; c < kCols / 16; ++c) {
       uint32_t b[4];
       ldmatrix4<true>(b, sw + wrow * 128 + (((2 * c + wcol) ^ (wrow & 7)) << 4));
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816(acc[mt][2 * c], xf[mt], b[0], b[1]);
-        mma16816(acc[mt][2 * c + 1], xf[mt], b[2], b[3]);
-      }
+      for (int e = 0; e < TERMS; ++e)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816(acc[mt][2 * c], xf[e][mt], b[0], b[1]);
+          mma16816(acc[mt][2 * c + 1], xf[e][mt], b[2], b[3]);
+        }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -283,9 +295,15 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
         *reinterpret_cast<__half2*>(p + a.N) = sat_half2(u, clamped);
         if (clamped) status_flag(a.status, kFlagF16Range);
       }
-      const float2 v = gate_act2(g, a.act);
-      *reinterpret_cast<__nv_bfloat162*>(a.out + static_cast<long long>(t) * a.N + col) =
-          __floats2bfloat162_rn(v.x * u.x, v.y * u.y);
+      const float2 h = __fmul2_rn(gate_act2(g, a.act), u);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(h.x, h.y);
+      __nv_bfloat16* p = a.out + static_cast<long long>(t) * a.N + col;
+      *reinterpret_cast<__nv_bfloat162*>(p) = hi;
+      if (a.M <= kThinTwoTermM) {
+        const float2 hf = __bfloat1622float2(hi);
+        *reinterpret_cast<__nv_bfloat162*>(p + static_cast<long long>(a.M) * a.N) =
+            __floats2bfloat162_rn(h.x - hf.x, h.y - hf.y);
+      }
     } else {
       float2 z = total(c / kCols, t, c % kCols);
       const float2 b = bias2(col);
@@ -308,11 +326,17 @@ int plan_split(int tiles, int K) {
       1, std::min<int64_t>({kMaxCluster, fit, steps / (kGroups * kMinSteps)})));
 }
 
-template <int MT, bool GLU>
+template <int MT, bool GLU, int TERMS>
 tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
-  constexpr int smem = Cfg<MT>::kBytes;
-  auto kern = thin_product<MT, GLU>;
+  constexpr int smem = Cfg<MT, TERMS>::kBytes;
+  auto kern = thin_product<MT, GLU, TERMS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // One carve-out for all of them: an SM that has to change it drains first, and
+  // the down product's blocks would not start beside the up product's (72 us
+  // for one token).
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
   if (e != cudaSuccess) return cuda_fail(e, "thin product smem");
   const int width = GLU ? kCols : 2 * kCols;
   const int tiles = (a.N + width - 1) / width;
@@ -349,7 +373,8 @@ tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
 
 template <bool GLU>
 tp_status launch_m(const ThinArgs& a, bool pdl, cudaStream_t stream) {
-  return a.M <= 16 ? launch<1, GLU>(a, pdl, stream) : launch<2, GLU>(a, pdl, stream);
+  if (!GLU && a.M <= kThinTwoTermM) return launch<1, GLU, GLU ? 1 : 2>(a, pdl, stream);
+  return a.M <= 16 ? launch<1, GLU, 1>(a, pdl, stream) : launch<2, GLU, 1>(a, pdl, stream);
 }
 
 }  // namespace

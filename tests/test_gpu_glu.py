@@ -1,7 +1,7 @@
 """The gated feed-forward block against fp64 (GPU).
 
-Tolerances follow the bf16 roundings (hs = 2^-8, half a step): H is rounded,
-so Z may be off by hs (|H| |Wd|) + hs |Z|.  In the backward G and U are rounded
+Tolerances follow the bf16 roundings (hs = 2^-8, half a step): H is rounded
+(up to 8 tokens its rest follows as a second term), so Z may be off by hs (|H| |Wd|) + hs |Z|.  In the backward G and U are rounded
 to fp16 (2^-11 of the value, half a step of 2^-24 below 2^-14), [dG | dU] and
 H to bf16: with their errors eG, eU, dG = dH U act'(G) may be off by |dH| (|act'| eU + |U| |act''| eG) and hs of itself (|act''| <= 1), dU and H
 likewise (|act'| <= 1.13), and the products follow by linearity.  fp32 sums
@@ -131,6 +131,19 @@ def test_forward_and_backward(case):
     d = make(M, h, f, bias)
     ref, tol = reference(d, kind)
     compare(run(d, t, kind), ref, tol)
+
+
+@pytest.mark.parametrize("M,h,f", [(1, 64, 96), (3, 200, 1000), (8, 1024, 2816)])
+def test_the_fewest_tokens_round_once(M, h, f):
+    """H crosses in two bf16 terms (2^-16 of it stays), so Z is off by its own
+    rounding and the fp32 terms of `reference` alone."""
+    d = make(M, h, f, True, seed=7)
+    Z = run(d, 1, "silu", save=False, backward=False)["Z"].double()
+    ref, tol = reference(d, "silu")
+    G, U = ref["GU"][:, :f], ref["GU"][:, f:]
+    cut = (HS - 2.0 ** -16) * ((act(G, "silu")[0] * U).abs() @ d["Wd"].double().abs())
+    bad = ((Z - ref["Z"]).abs() - (tol["Z"] - cut)).max().item()
+    assert bad <= 0, f"{bad:.3e} over the bound"
 
 
 @pytest.mark.parametrize("tile", ["128", "192", "256", "pair"])
