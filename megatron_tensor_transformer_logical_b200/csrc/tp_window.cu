@@ -59,8 +59,8 @@ namespace tp {
 namespace {
 
 constexpr int kBM = 128;  // query rows per tile
-constexpr int kBN = 128;  // keys per block (forward), keys per tile (dK / dV)
-constexpr int kB64 = 64;  // keys per block (dQ), queries per block (dK / dV)
+constexpr int kBN = 128;  // keys per tile (dK / dV)
+constexpr int kB64 = 64;  // keys per block (forward, dQ), queries per block (dK / dV)
 constexpr int kThreads = 384;
 constexpr float kRescaleLog2 = 8.0f;  // O keeps a stale maximum up to 2^8 behind
 constexpr float kCheckSum = 255.0f;   // a row sum above this may hide such a key
@@ -109,8 +109,6 @@ struct WinArgs {
   int heads, kv_heads, group;
   int window, sinks;  // both clamped to sk
   float scale, scale_log2;
-  void* o;
-  long long ldo;
   float* lse;  // [b, heads, sq]
   // backward
   const float* nlse;  // -LSE * log2(e) and -D: [b * heads] rows of sp floats,
@@ -218,7 +216,7 @@ struct RowMask {
 // Whether all rows of a tile, positions [p0, p0 + 128), see all of the key
 // block at k0.
 __device__ __forceinline__ bool all_visible(int p0, int k0, const WinArgs& a) {
-  return k0 + kBN - 1 <= p0 && (k0 > p0 + kBM - 1 - a.window || k0 + kBN <= a.sinks);
+  return k0 + kB64 - 1 <= p0 && (k0 > p0 + kBM - 1 - a.window || k0 + kB64 <= a.sinks);
 }
 
 // Row with query position p (p < sk) in the key block that starts at k0.
@@ -234,7 +232,7 @@ __device__ __forceinline__ RowMask row_mask(int p, int k0, const WinArgs& a) {
 __device__ __forceinline__ float row_max_masked(uint32_t srow, const RowMask& m) {
   float mx = -INFINITY;
 #pragma unroll
-  for (int c = 0; c < kBN; c += 32) {
+  for (int c = 0; c < kB64; c += 32) {
     float v[32];
     tmem_ld32(srow + c, v);
     if (!m.full(c)) {
@@ -256,7 +254,7 @@ __device__ __forceinline__ float row_max_masked(uint32_t srow, const RowMask& m)
 // save.)
 template <bool BF, bool ALL>
 __device__ __forceinline__ float exp_row(uint32_t srow, const RowMask& mask, float scale_log2,
-                                         float m, uint32_t (&pk)[kBN / 2]) {
+                                         float m, uint32_t (&pk)[kB64 / 2]) {
   const float2 sc2 = make_float2(scale_log2, scale_log2), nm2 = make_float2(-m, -m);
   float2 acc = make_float2(0.0f, 0.0f);
   // The next chunk's tensor-memory load is in flight while this one is
@@ -265,11 +263,11 @@ __device__ __forceinline__ float exp_row(uint32_t srow, const RowMask& mask, flo
   tmem_ld32_nowait(srow, nx);
   tmem_wait_ld(nx);
 #pragma unroll
-  for (int c = 0; c < kBN; c += 32) {
+  for (int c = 0; c < kB64; c += 32) {
     float v[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(nx[i]);
-    if (c + 32 < kBN) tmem_ld32_nowait(srow + c + 32, nx);
+    if (c + 32 < kB64) tmem_ld32_nowait(srow + c + 32, nx);
     const uint32_t vis = ALL ? 0xffffffffu : mask.bits(c);
     if (ALL || __any_sync(0xffffffffu, vis != 0u)) {
       float2 u[16];
@@ -292,7 +290,7 @@ __device__ __forceinline__ float exp_row(uint32_t srow, const RowMask& mask, flo
 #pragma unroll
       for (int i = 0; i < 16; ++i) pk[c / 2 + i] = 0u;
     }
-    if (c + 32 < kBN) tmem_wait_ld(nx);
+    if (c + 32 < kB64) tmem_wait_ld(nx);
   }
   return acc.x + acc.y;
 }
@@ -314,34 +312,38 @@ __device__ __forceinline__ uint32_t k_off(int kk, int rows) {
 
 template <int DH>
 struct FwdSmem {
-  static constexpr int kTile = 128 * DH * 2;
-  static constexpr int kBytes = 1024 + 6 * kTile + 256;  // Q[2], K[2], V[2], barriers
+  static constexpr int kStages = 4;
+  static constexpr int kTile = kBM * DH * 2, kTile64 = kB64 * DH * 2;
+  // Q[2], ring of (K, V), barriers
+  static constexpr int kBytes = 1024 + 2 * kTile + 2 * kStages * kTile64 + 256;
 };
 
-// One CTA per (sequence, head, pair of adjacent 128-row query tiles), as in
-// the full causal core: warp 0 TMA, warp 1 tensor memory and MMA issue, warps
-// 4-7 / 8-11 the softmax of tile 0 / 1.
+// One CTA per (sequence, head, pair of adjacent 128-row query tiles): warp 0
+// TMA, warp 1 tensor memory, warps 1 / 2 the MMA issue and warps 4-7 / 8-11 the
+// softmax of tile 0 / 1.  Blocks of 64 keys, so that tensor memory holds two S per tile
+// beside O: the next block's S is there when a block's P has been given, and
+// the softmax does not wait for the products.  With one S of 128 keys it did
+// for 1740 of 4400 clocks a block.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-               const __grid_constant__ CUtensorMap tmV, const WinArgs a) {
-  constexpr int kTile = FwdSmem<DH>::kTile;
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+               const WinArgs a) {
+  using C = FwdSmem<DH>;
+  constexpr int kTile = C::kTile, kTile64 = C::kTile64, kSt = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;              // [2] query tiles
-  uint8_t* sK = smem + 2 * kTile;  // [2] stages
-  uint8_t* sV = smem + 4 * kTile;  // [2] stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 6 * kTile);
-  uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;   // [2] stages
-  uint64_t* k_empty = bars + 3;  // [2]
-  uint64_t* v_full = bars + 5;   // [2]
-  uint64_t* v_empty = bars + 7;  // [2]
-  uint64_t* s_full = bars + 9;   // [2] tiles: S ready (and the previous P V done)
-  uint64_t* p_full = bars + 11;  // [2] tiles: P stored (and O rescaled)
-  uint64_t* o_full = bars + 13;  // [2] tiles: P V done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 15);
+  uint8_t* sQ = smem;               // [2] query tiles, at the end O
+  uint8_t* sKV = sQ + 2 * kTile;    // stage st: K at +0, V at +kTile64
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kSt * 2 * kTile64);
+  uint64_t* kv_full = bars;          // [4] stages
+  uint64_t* kv_empty = bars + 4;     // [4]
+  uint64_t* s_full = bars + 8;       // [tile][buffer]: S ready
+  uint64_t* p_full = bars + 12;      // [tile][buffer]: P stored (and O rescaled)
+  uint64_t* o_full = bars + 16;      // [tile][buffer]: the buffer's P V done
+  uint64_t* q_full = bars + 20;      // [2] tiles
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int npairs = ((a.sq + kBM - 1) / kBM + 1) / 2;
@@ -349,19 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head = blockIdx.x % a.heads, bi = blockIdx.x / a.heads;
   const int kvh = head / a.group;
   const int r0 = 2 * pair * kBM;
-  const BlockList<kBN> bl(r0, a);
+  const BlockList<kB64> bl(r0, a);
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 2);  // both tiles' products
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);  // one arrival per warp of the tile's softmax group
       mbar_init(&o_full[i], 1);
     }
+    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  // Tile x: S_x at columns [256 x, +128) (P_x over its first 64), O_x at
-  // [256 x + 128, + DH).
-  auto tS = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x); };
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);  // uniform
+  // Tile x, buffer b (the parity of the block's place in the list): S at
+  // columns [256 x + 64 b, + 64), P over its first 32; O at [256 x + 128, + DH).
+  auto tS = [tmem](int x, int b) { return tmem + static_cast<uint32_t>(256 * x + 64 * b); };
   auto tO = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
 
   if (warp == 0) {
@@ -384,106 +384,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
-      const int tiles = r0 + kBM < a.sq ? 2 : 1;
-      mbar_arrive_expect_tx(q_full, tiles * kTile);
-      for (int x = 0; x < tiles; ++x)
-        load_tile<DH>(sQ + x * kTile, &tmQ, q_full, head, r0 + x * kBM, bi, 128);
+      tma_prefetch_desc(&tmO);
+      auto load_q = [&](int x) {
+        mbar_arrive_expect_tx(&q_full[x], kTile);
+        load_tile<DH>(sQ + x * kTile, &tmQ, &q_full[x], head, r0 + x * kBM, bi, kBM);
+      };
+      load_q(0);
       for (int j = 0; j < bl.n && ok; ++j) {
-        const int st = j & 1;
-        const uint32_t ph = static_cast<uint32_t>(j >> 1) & 1u;
-        const int krow = bl.block(j) * kBN;
-        if (!(ok = mbar_wait(&k_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
-        mbar_arrive_expect_tx(&k_full[st], kTile);
-        load_tile<DH>(sK + st * kTile, &tmK, &k_full[st], kvh, krow, bi, 128);
-        if (!(ok = mbar_wait(&v_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
-        mbar_arrive_expect_tx(&v_full[st], kTile);
-        load_tile<DH>(sV + st * kTile, &tmV, &v_full[st], kvh, krow, bi, 128);
+        const int st = j % kSt;
+        const uint32_t ph = static_cast<uint32_t>(j / kSt) & 1u;
+        const int krow = bl.block(j) * kB64;
+        uint8_t* dst = sKV + st * (2 * kTile64);
+        if (!(ok = mbar_wait(&kv_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
+        mbar_arrive_expect_tx(&kv_full[st], 2 * kTile64);
+        load_tile<DH>(dst, &tmK, &kv_full[st], kvh, krow, bi, kB64);
+        load_tile<DH>(dst + kTile64, &tmV, &kv_full[st], kvh, krow, bi, kB64);
+        if (j == 0 && r0 + kBM < a.sq) load_q(1);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && bl.n > 0) {
-      // --------------------------------------------------------- MMA issuer
-      // Per listed block j and tile that sees it: P_x V_j; then S_x of block
-      // j + 1 if the tile sees that.  The MMAs run in issue order, so S_x
-      // overwrites P_x only after its product has read it, and the commit of
-      // S_x also covers the tile's previous P V.
-      constexpr uint32_t kIdS = idesc<BF>(128, 128, false, false);  // Q K^T
-      constexpr uint32_t kIdO = idesc<BF>(128, DH, false, true);    // P V
-      auto issue_s = [&](int x, int j) {
-        const uint32_t q_addr = smem_u32(sQ + x * kTile);
-        const uint32_t k_addr = smem_u32(sK + (j & 1) * kTile);
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          umma_bf16(tS(x), sw128_desc(q_addr + k_off(kk, 128), 16, 1024),
-                    sw128_desc(k_addr + k_off(kk, 128), 16, 1024), kIdS, kk > 0 ? 1u : 0u);
-        umma_commit(&s_full[x]);
-      };
-      int done[2] = {0, 0};  // P V products issued per tile
-      bool ok = mbar_wait(q_full, 0, a.status, kStatusAttnTimeout);
-      for (int j = -1; j < bl.n && ok; ++j) {
-        const int st = j & 1;
-        if (j >= 0 && !(ok = mbar_wait(&v_full[st], static_cast<uint32_t>(j >> 1) & 1u, a.status,
-                                       kStatusAttnTimeout)))
-          break;
-        const bool more = j + 1 < bl.n;
-        bool k_next = false;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          if (!ok) break;
-          if (j >= 0 && bl.sees(x, j)) {
-            if (!(ok = mbar_wait(&p_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
-                                 kStatusAttnTimeout)))
-              break;
+  } else if (warp <= 2) {
+    if (bl.n > 0) {
+      // -------------------------------------------------- MMA issuer of a tile
+      // Per listed block j that the tile sees: P V_j; then S of block j + 2, in
+      // the same buffer.  The MMAs run in issue order, so S overwrites P only
+      // after its product has read it.  An issuer of its own per tile: one for
+      // both was busy for 1.5 times as long as its products ran, most of it
+      // waiting for one tile while the other's P was there.
+      constexpr uint32_t kIdS = idesc<BF>(kBM, kB64, false, false);  // Q K^T
+      constexpr uint32_t kIdO = idesc<BF>(kBM, DH, false, true);     // P V
+      const int x = warp - 1;
+      const uint32_t q_addr = smem_u32(sQ + x * kTile);
+      uint32_t pbits = 0u;  // bit b: parity of p_full[x][b]'s next wait
+      bool some = false;    // a P V product has been issued
+      bool ok = bl.count(x) == 0 ||
+                warp_mbar_wait(&q_full[x], 0, a.status, kStatusAttnTimeout);
+      for (int j = -2; j < bl.n && ok; ++j) {
+        const int b = j & 1;
+        const int jn = j + 2, st = j & (kSt - 1), stn = jn & (kSt - 1);
+        if (j >= 0 && bl.sees(x, j)) {
+          if (!(ok = warp_mbar_wait(&p_full[2 * x + b], (pbits >> b) & 1u, a.status,
+                                    kStatusAttnTimeout)))
+            break;
+          pbits ^= 1u << b;
+          tc_fence_after();
+          const uint32_t v_addr = smem_u32(sKV + st * (2 * kTile64) + kTile64);
+          warp_umma_ts4(tO(x), tS(x, b), sw128_desc(v_addr, kB64 * 128, 1024), kIdO,
+                        some ? 1u : 0u);
+          warp_umma_commit(&o_full[2 * x + b]);
+          some = true;
+        }
+        if (j >= 0) warp_umma_commit(&kv_empty[st]);
+        if (jn < bl.n) {
+          // Waited for whether seen or not: an issuer that skipped blocks would
+          // release a stage twice.
+          if (!(ok = warp_mbar_wait(&kv_full[stn], static_cast<uint32_t>(jn / kSt) & 1u, a.status,
+                                    kStatusAttnTimeout)))
+            break;
+          if (bl.sees(x, jn)) {
             tc_fence_after();
-            const uint32_t v_addr = smem_u32(sV + st * kTile);
+            const uint32_t k_addr = smem_u32(sKV + stn * (2 * kTile64));
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)  // 16 keys: 8 columns of pairs
-              umma_f16_ts(tO(x), tS(x) + static_cast<uint32_t>(kk * 8),
-                          sw128_desc(v_addr + kk * 16 * 128, 128 * 128, 1024), kIdO,
-                          (done[x] > 0 || kk > 0) ? 1u : 0u);
-            umma_commit(&o_full[x]);
-            ++done[x];
-          }
-          if (more && bl.sees(x, j + 1)) {
-            if (!k_next) {
-              if (!(ok = mbar_wait(&k_full[(j + 1) & 1], static_cast<uint32_t>((j + 1) >> 1) & 1u,
-                                   a.status, kStatusAttnTimeout)))
-                break;
-              tc_fence_after();
-              k_next = true;
-            }
-            issue_s(x, j + 1);
+            for (int c = 0; c < DH / 64; ++c)
+              warp_umma_ss4(tS(x, b), sw128_desc(q_addr + c * kBM * 128, 16, 1024),
+                            sw128_desc(k_addr + c * kB64 * 128, 16, 1024), kIdS, c > 0 ? 1u : 0u);
+            warp_umma_commit(&s_full[2 * x + b]);
           }
         }
-        if (!ok) break;
-        if (more) umma_commit(&k_empty[(j + 1) & 1]);
-        if (j >= 0) umma_commit(&v_empty[st]);
       }
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;
-    const int r = r0 + x * kBM + quarter * 32 + lane;
+    const int row0 = r0 + x * kBM + quarter * 32, r = row0 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t srow = tS(x) + lane_off, orow_t = tO(x) + lane_off;
+    const uint32_t orow_t = tO(x) + lane_off;
     // Rows past the end take the last position: their results are not stored.
     const int p = min(r, a.sq - 1) + a.off;
     const int total = bl.count(x);
     float m_used = -INFINITY, l_run = 0.0f;
     bool ok = true;
-    int cnt = 0;
+    int cnt = 0, last = 0;   // blocks so far; the buffer of the last one
+    uint32_t bits = 0u;      // bit b: parity of s_full[x][b]'s next wait
+    // The buffer's P V, by the parity its S had.
+    auto wait_o = [&](int b) {
+      const bool done = mbar_wait(&o_full[2 * x + b], ((bits >> b) & 1u) ^ 1u, a.status,
+                                  kStatusAttnTimeout);
+      if (done) tc_fence_after();
+      return done;
+    };
     for (int j = 0; j < bl.n && cnt < total; ++j) {
       if (!bl.sees(x, j)) continue;
-      if (!(ok = mbar_wait(&s_full[x], static_cast<uint32_t>(cnt) & 1u, a.status,
-                           kStatusAttnTimeout)))
+      const int b = j & 1;
+      const uint32_t srow = tS(x, b) + lane_off;
+      if (!(ok = mbar_wait(&s_full[2 * x + b], (bits >> b) & 1u, a.status, kStatusAttnTimeout)))
         break;
+      bits ^= 1u << b;
       tc_fence_after();
-      const int k0 = bl.block(j) * kBN;
+      const int k0 = bl.block(j) * kB64;
       const RowMask mask = row_mask(p, k0, a);
       const bool all = all_visible(r0 + x * kBM + a.off, k0, a);
-      if (cnt == 0) m_used = row_max_masked(srow, mask) * a.scale_log2;
-      uint32_t pk[kBN / 2];
+      // A warp none of whose rows has seen a key yet takes the exact maximum.
+      const bool first = __all_sync(0xffffffffu, m_used == -INFINITY);
+      if (first) m_used = row_max_masked(srow, mask) * a.scale_log2;
+      uint32_t pk[kB64 / 2];
       // A row that has seen no key yet (m_used = -inf) has P = 0 by the mask;
       // 0 stands in for its maximum.
       float rs = all ? exp_row<BF, true>(srow, mask, a.scale_log2,
@@ -493,17 +497,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The first block set the maximum in use, so its P <= 1.  Later blocks:
       // a row sum above kCheckSum, or a row without a maximum so far, sends
       // the warp to the exact maximum.
-      if (cnt > 0 && __any_sync(0xffffffffu, rs > kCheckSum || m_used == -INFINITY)) {
+      if (!first && __any_sync(0xffffffffu, rs > kCheckSum || m_used == -INFINITY)) {
         const float m_new = row_max_masked(srow, mask) * a.scale_log2;
         const bool need = m_new > m_used + kRescaleLog2;
         if (__any_sync(0xffffffffu, need)) {
           // Recompute P at the new maximum (S is intact: P has not been
-          // stored) and rescale O (the tile's previous P V completed before
-          // this S) and l.  From -inf the factor is 0, on sums that are 0.
+          // stored) and rescale O, once the previous P V is done, and l.
+          // From -inf the factor is 0, on sums that are 0.
           const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
           if (need) m_used = m_new;
           rs = exp_row<BF, false>(srow, mask, a.scale_log2,
                                   m_used == -INFINITY ? 0.0f : m_used, pk);
+          if (!(ok = last == b ? true : wait_o(last))) break;
 #pragma unroll 1
           for (int c = 0; c < DH; c += 32) {
             float o[32];
@@ -517,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       l_run += rs;
 #pragma unroll
-      for (int c = 0; c < kBN / 2; c += 16) {
+      for (int c = 0; c < kB64 / 2; c += 16) {
         uint32_t q16[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) q16[i] = pk[c + i];
@@ -526,19 +531,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[x]);
+      if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
+      last = b;
       ++cnt;
     }
-    if (ok && total > 0)
-      ok = mbar_wait(&o_full[x], static_cast<uint32_t>(total - 1) & 1u, a.status,
-                     kStatusAttnTimeout);
+    if (ok && total > 0) ok = wait_o(last);
+    if (ok && total == 0 && bl.n > 0 && r0 + x * kBM < a.sq)
+      ok = mbar_wait(&q_full[x], 0, a.status, kStatusAttnTimeout);
     if (ok) {
-      if (total > 0) tc_fence_after();
+      // O through the warp's rows of the query tile, which has landed and been
+      // read by every product by now.
       const bool some = l_run > 0.0f;
       const float inv = some ? 1.0f / l_run : 0.0f;
-      uint8_t* orow = static_cast<uint8_t*>(a.o) +
-                      ((static_cast<long long>(bi) * a.sq + r) * a.ldo + head * DH) * 2;
-#pragma unroll 1
+      uint8_t* box = sQ + x * kTile + quarter * 32 * 128;
+#pragma unroll
       for (int c = 0; c < DH; c += 32) {
         float v[32];
         if (total > 0) tmem_ld32(orow_t + c, v);
@@ -546,15 +552,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.0f;
         }
-        if (r < a.sq) {
+        uint8_t* dst = box + (c >> 6) * kBM * 128 + lane * 128;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(orow + 2 * (c + 8 * q)) = pack8t<BF>(v + 8 * q, inv);
-        }
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(dst + ((((c & 63) / 8 + q) ^ (lane & 7)) << 4)) =
+              pack8t<BF>(v + 8 * q, inv);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0 && row0 < a.sq) {
+#pragma unroll
+        for (int c = 0; c < DH / 64; ++c)
+          tma_store_3d(&tmO, box + c * kBM * 128, head * DH + 64 * c, row0, bi);
+        bulk_commit();
       }
       if (r < a.sq)
         a.lse[(static_cast<long long>(bi) * a.heads + head) * a.sq + r] =
             some ? (m_used + log2f(l_run)) * kLn2 : -INFINITY;
+      if (lane == 0) bulk_wait_read<0>();
     }
   }
 
@@ -1512,16 +1527,15 @@ tp_status smem_opt_in(K kern, int bytes, const char* what) {
 
 template <bool BF, int DH>
 tp_status fwd(const WindowAttn& w, cudaStream_t stream) {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   const int64_t nq = int64_t(w.heads) * DH, nk = int64_t(w.kv_heads) * DH;
   if (!make_map3(&q, w.q, BF, nq, w.sq, w.b, w.ldq, 128) ||
-      !make_map3(&k, w.k, BF, nk, w.sk, w.b, w.ldk, 128) ||
-      !make_map3(&v, w.v, BF, nk, w.sk, w.b, w.ldv, 128))
+      !make_map3(&k, w.k, BF, nk, w.sk, w.b, w.ldk, kB64) ||
+      !make_map3(&v, w.v, BF, nk, w.sk, w.b, w.ldv, kB64) ||
+      !make_map3(&o, w.o, BF, nq, w.sq, w.b, w.ldo, 32))
     return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (window attention)");
   WinArgs a = base_args(w);
   if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
-  a.o = const_cast<void*>(w.o);
-  a.ldo = w.ldo;
   a.lse = const_cast<float*>(w.lse);
   constexpr int smem = FwdSmem<DH>::kBytes;
   if (tp_status s = smem_opt_in(window_fwd<BF, DH>, smem, "window attention smem"); s != TP_OK)
@@ -1531,7 +1545,7 @@ tp_status fwd(const WindowAttn& w, cudaStream_t stream) {
   {
     LaunchScope scope(TP_KIND_ATTN_FWD, 4.0 * DH * visible_pairs(w),
                       4.0 * double(w.b) * (w.sq * nq + w.sk * nk), stream);
-    window_fwd<BF, DH><<<grid, kThreads, smem, stream>>>(q, k, v, a);
+    window_fwd<BF, DH><<<grid, kThreads, smem, stream>>>(q, k, v, o, a);
   }
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? TP_OK : cuda_fail(e, "window attention forward launch");
