@@ -96,8 +96,9 @@ __device__ __forceinline__ void warp_umma_ss4(uint32_t d_tmem, uint64_t adesc, u
       : "memory");
 }
 
-// The same with A in tensor memory (16 columns of A in 8) and B an MN-major
-// tile (16 rows of 128 bytes).
+// The same with A in tensor memory, 16 columns of A in 8, the second 32 of them
+// HALF columns on, and B an MN-major tile (16 rows of 128 bytes).
+template <int HALF = 16>
 __device__ __forceinline__ void warp_umma_ts4(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                               uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -108,11 +109,11 @@ __device__ __forceinline__ void warp_umma_ts4(uint32_t d_tmem, uint32_t a_tmem, 
       "setp.eq.b32 p, %4, %4;\n\t"
       "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+      "add.s32 a, %1, %5;\n\tadd.s64 b, %2, 256;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-      "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+      "add.s32 a, %1, %6;\n\tadd.s64 b, %2, 384;\n\t"
       "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(HALF), "n"(HALF + 8)
       : "memory");
 }
 

@@ -305,11 +305,6 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
     tma_load_3d(dst + c * rows * 128, map, bar, head * DH + 64 * c, row, seq);
 }
 
-// Byte offset of K step kk (16 columns) in a K-major tile of `rows` rows.
-__device__ __forceinline__ uint32_t k_off(int kk, int rows) {
-  return static_cast<uint32_t>((kk >> 2) * rows * 128 + (kk & 3) * 32);
-}
-
 template <int DH>
 struct FwdSmem {
   static constexpr int kStages = 4;
@@ -711,7 +706,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);  // uniform
   pdl_next();
   pdl_wait();  // the row terms
   // Tile x: S_x at [256 x, +64) (dS_x over its first 32 columns), dP_x at
@@ -746,7 +741,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && bl.n > 0) {
+    if (bl.n > 0) {
       constexpr uint32_t kIdSP = idesc<BF>(128, 64, false, false);  // Q K^T, dO V^T
       constexpr uint32_t kIdQ = idesc<BF>(128, DH, false, true);    // dS K
       auto issue_sp = [&](int x, int j) {
@@ -754,17 +749,17 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
         const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
         const uint32_t v_addr = k_addr + kTile64;
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          umma_bf16(tS(x), sw128_desc(q_addr + k_off(kk, 128), 16, 1024),
-                    sw128_desc(k_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
-          umma_bf16(tP(x), sw128_desc(do_addr + k_off(kk, 128), 16, 1024),
-                    sw128_desc(v_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+        for (int c = 0; c < DH / 64; ++c) {
+          warp_umma_ss4(tS(x), sw128_desc(q_addr + c * kBM * 128, 16, 1024),
+                        sw128_desc(k_addr + c * kB64 * 128, 16, 1024), kIdSP, c > 0 ? 1u : 0u);
+          warp_umma_ss4(tP(x), sw128_desc(do_addr + c * kBM * 128, 16, 1024),
+                        sw128_desc(v_addr + c * kB64 * 128, 16, 1024), kIdSP, c > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[x]);
+        warp_umma_commit(&s_full[x]);
       };
       const int total[2] = {bl.count(0), bl.count(1)};
       int done[2] = {0, 0};
-      bool ok = mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
+      bool ok = warp_mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
       auto issue = [&](auto two) {
         for (int j = -1; j < bl.n && ok; ++j) {
           const bool more = j + 1 < bl.n;
@@ -773,28 +768,20 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
           for (int x = 0; x < 2; ++x) {
             if (!ok) break;
             if (j >= 0 && bl.sees(x, j)) {
-              if (!(ok = mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
+              if (!(ok = warp_mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
                                    kStatusAttnTimeout)))
                 break;
               tc_fence_after();
               const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
-#pragma unroll
-              for (int kk = 0; kk < kB64 / 16; ++kk)
-                umma_f16_ts(tQ(x), tS(x) + static_cast<uint32_t>(kk * 8),
-                            sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ,
-                            (done[x] > 0 || kk > 0) ? 1u : 0u);
-              if constexpr (two) {
-#pragma unroll
-                for (int kk = 0; kk < kB64 / 16; ++kk)
-                  umma_f16_ts(tQ(x), tP(x) + static_cast<uint32_t>(kk * 8),
-                              sw128_desc(k_addr + kk * 2048, 64 * 128, 1024), kIdQ, 1u);
-              }
-              if (++done[x] == total[x]) umma_commit(&dq_done[x]);
+              const uint64_t kd = sw128_desc(k_addr, 64 * 128, 1024);
+              warp_umma_ts4(tQ(x), tS(x), kd, kIdQ, done[x] > 0 ? 1u : 0u);
+              if constexpr (two) warp_umma_ts4(tQ(x), tP(x), kd, kIdQ, 1u);
+              if (++done[x] == total[x]) warp_umma_commit(&dq_done[x]);
             }
             if (more && bl.sees(x, j + 1)) {
               if (!kv_next) {
                 const int ks = (j + 1) % kKvStages;
-                if (!(ok = mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
+                if (!(ok = warp_mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
                                      a.status, kStatusAttnTimeout)))
                   break;
                 tc_fence_after();
@@ -804,7 +791,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
             }
           }
           if (!ok) break;
-          if (j >= 0) umma_commit(&kv_empty[j % kKvStages]);
+          if (j >= 0) warp_umma_commit(&kv_empty[j % kKvStages]);
         }
       };
       if (two_terms)
@@ -1056,7 +1043,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);  // uniform
   pdl_next();
   pdl_wait();  // the row terms
   // S^T buffers at columns 0 and 64, dP^T at 128 and 192, dV at 256, dK at 384.
@@ -1108,7 +1095,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdSP = idesc<BF>(128, 64, false, false);  // K Q^T, V dO^T
       constexpr uint32_t kIdAcc = idesc<BF>(128, DH, false, true);  // P^T dO, dS^T Q
       const uint32_t k_addr = smem_u32(sK), v_addr = smem_u32(sV);
@@ -1117,20 +1104,20 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
       auto issue_sp = [&](long long gg) -> bool {
         const int st = static_cast<int>(gg & 1);
         const int qs = static_cast<int>(gg % kQdStages);
-        if (!mbar_wait(&qd_full[qs], static_cast<uint32_t>(gg / kQdStages) & 1u, a.status,
+        if (!warp_mbar_wait(&qd_full[qs], static_cast<uint32_t>(gg / kQdStages) & 1u, a.status,
                        kStatusAttnTimeout))
           return false;
         tc_fence_after();
         const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
         const uint32_t do_addr = q_addr + kTile64;
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-          umma_bf16(tS(st), sw128_desc(k_addr + k_off(kk, 128), 16, 1024),
-                    sw128_desc(q_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
-          umma_bf16(tP(st), sw128_desc(v_addr + k_off(kk, 128), 16, 1024),
-                    sw128_desc(do_addr + k_off(kk, 64), 16, 1024), kIdSP, kk > 0 ? 1u : 0u);
+        for (int c = 0; c < DH / 64; ++c) {
+          warp_umma_ss4(tS(st), sw128_desc(k_addr + c * kBN * 128, 16, 1024),
+                        sw128_desc(q_addr + c * kB64 * 128, 16, 1024), kIdSP, c > 0 ? 1u : 0u);
+          warp_umma_ss4(tP(st), sw128_desc(v_addr + c * kBN * 128, 16, 1024),
+                        sw128_desc(do_addr + c * kB64 * 128, 16, 1024), kIdSP, c > 0 ? 1u : 0u);
         }
-        umma_commit(&s_full[st]);
+        warp_umma_commit(&s_full[st]);
         return true;
       };
       bool ok = true;
@@ -1142,51 +1129,39 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
         const KvItem it = kv_item(k, a);
         const int len = it.j1 - it.j0;
         if (len <= 0) continue;
-        if (!(ok = mbar_wait(kv_full, it_no & 1u, a.status, kStatusAttnTimeout))) break;
+        if (!(ok = warp_mbar_wait(kv_full, it_no & 1u, a.status, kStatusAttnTimeout))) break;
         if (!(ok = issue_sp(g))) break;
-        if (len == 1) umma_commit(kv_empty);
+        if (len == 1) warp_umma_commit(kv_empty);
         auto issue = [&](auto two) {
           for (int j = 0; j < len; ++j) {
             const long long gj = g + j;
             if (j + 1 < len) {
               if (!(ok = issue_sp(gj + 1))) break;
-              if (j + 2 == len) umma_commit(kv_empty);  // the item's last S^T / dP^T
+              if (j + 2 == len) warp_umma_commit(kv_empty);  // the item's last S^T / dP^T
             }
             const int st = static_cast<int>(gj & 1);
-            if (!(ok = mbar_wait(&p_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+            if (!(ok = warp_mbar_wait(&p_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
                                  kStatusAttnTimeout)))
               break;
             // The item's first products overwrite the accumulators: the previous
             // item's epilogue must have read them.
             if (j == 0 && it_no > 0 &&
-                !(ok = mbar_wait(acc_empty, (it_no - 1u) & 1u, a.status, kStatusAttnTimeout)))
+                !(ok = warp_mbar_wait(acc_empty, (it_no - 1u) & 1u, a.status, kStatusAttnTimeout)))
               break;
             tc_fence_after();
             const int qs = static_cast<int>(gj % kQdStages);
             const uint32_t q_addr = smem_u32(sQdO + qs * (2 * kTile64));
             const uint32_t do_addr = q_addr + kTile64;
-#pragma unroll
-            for (int kk = 0; kk < kB64 / 16; ++kk) {
-              // queries [16 kk, 16 kk + 16): group kk / 2's columns, 8 columns each
-              const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1));
-              const uint32_t acc = (j | kk) != 0 ? 1u : 0u;
-              umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
-                          kIdAcc, acc);
-              umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
-                          kIdAcc, acc);
-            }
+            // 32 queries lie 32 columns apart, their second terms 16 columns on
+            const uint64_t dod = sw128_desc(do_addr, 64 * 128, 1024);
+            const uint64_t qd = sw128_desc(q_addr, 64 * 128, 1024);
+            warp_umma_ts4<32>(tdV, tS(st), dod, kIdAcc, j > 0 ? 1u : 0u);
+            warp_umma_ts4<32>(tdK, tP(st), qd, kIdAcc, j > 0 ? 1u : 0u);
             if constexpr (two) {
-              // the second terms, 16 columns on
-#pragma unroll
-              for (int kk = 0; kk < kB64 / 16; ++kk) {
-                const uint32_t col = static_cast<uint32_t>(32 * (kk >> 1) + 8 * (kk & 1) + 16);
-                umma_f16_ts(tdV, tS(st) + col, sw128_desc(do_addr + kk * 2048, 64 * 128, 1024),
-                            kIdAcc, 1u);
-                umma_f16_ts(tdK, tP(st) + col, sw128_desc(q_addr + kk * 2048, 64 * 128, 1024),
-                            kIdAcc, 1u);
-              }
+              warp_umma_ts4<32>(tdV, tS(st) + 16, dod, kIdAcc, 1u);
+              warp_umma_ts4<32>(tdK, tP(st) + 16, qd, kIdAcc, 1u);
             }
-            umma_commit(&qd_empty[qs]);
+            warp_umma_commit(&qd_empty[qs]);
           }
         };
         if (it.two)
@@ -1194,7 +1169,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
         else
           issue(std::false_type{});
         if (!ok) break;
-        umma_commit(acc_done);
+        warp_umma_commit(acc_done);
         g += len;
         ++it_no;
       }
