@@ -132,6 +132,17 @@ __device__ __forceinline__ bool warp_mbar_wait(uint64_t* bar, uint32_t parity, c
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, w, code));
 }
 
+// The block's last barrier.  Where a wait has given up, copies and products may
+// still be under way: they get 200 us (they take a few) before tensor memory
+// is freed and the block leaves its shared memory.
+__device__ __forceinline__ void leave(bool gave_up) {
+  if (__syncthreads_or(gave_up)) {
+    const unsigned long long t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) __nanosleep(1000);
+    __syncthreads();
+  }
+}
+
 // 3-D tiled load of one box (columns x, rows y of sequence z) into shared
 // memory; completion is signalled on `bar` through its transaction count.
 __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,

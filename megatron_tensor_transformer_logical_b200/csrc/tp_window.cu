@@ -309,16 +309,43 @@ template <int DH>
 struct FwdSmem {
   static constexpr int kStages = 4;
   static constexpr int kTile = kBM * DH * 2, kTile64 = kB64 * DH * 2;
-  // Q[2], ring of (K, V), barriers
-  static constexpr int kBytes = 1024 + 2 * kTile + 2 * kStages * kTile64 + 256;
+  static constexpr int kBox = 32 * 128;  // 32 rows x 64 columns of O, per softmax warp
+  // Q[2], ring of (K, V), O boxes, barriers
+  static constexpr int kBytes = 1024 + 2 * kTile + 2 * kStages * kTile64 + 8 * kBox + 256;
 };
 
-// One CTA per (sequence, head, pair of adjacent 128-row query tiles): warp 0
-// TMA, warp 1 tensor memory, warps 1 / 2 the MMA issue and warps 4-7 / 8-11 the
-// softmax of tile 0 / 1.  Blocks of 64 keys, so that tensor memory holds two S per tile
-// beside O: the next block's S is there when a block's P has been given, and
-// the softmax does not wait for the products.  With one S of 128 keys it did
-// for 1740 of 4400 clocks a block.
+// The t-th item of this CTA, or r0 = -1: rounds of one item per CTA in snake
+// order, longest rows first, heads fastest.
+struct FwdItem {
+  int r0, head, bi;
+  __device__ __forceinline__ FwdItem(int t, const WinArgs& a) {
+    const long long n = gridDim.x, c = blockIdx.x;
+    const long long k = t * n + ((t & 1) ? n - 1 - c : c);
+    const int bh = a.bkv * a.group;
+    r0 = -1;
+    if (k >= a.items) return;
+    const int pair = static_cast<int>(k / bh);
+    const int h = static_cast<int>(k - static_cast<long long>(pair) * bh);
+    r0 = 2 * kBM * (a.items / bh - 1 - pair);
+    head = h % a.heads;
+    bi = h / a.heads;
+  }
+  // whether query tile x is loaded (n: the item's blocks)
+  __device__ __forceinline__ bool has_q(int x, int n, const WinArgs& a) const {
+    return n > 0 && r0 + x * kBM < a.sq;
+  }
+};
+
+// Persistent: a CTA per SM walks items of (sequence, head, pair of adjacent
+// 128-row query tiles), warp 0 TMA, warp 1 tensor memory, warps 1 / 2 the MMA
+// issue and warps 4-7 / 8-11 the softmax of tile 0 / 1.  Blocks of 64 keys, so
+// that tensor memory holds two S per tile beside O: the next block's S is
+// there when a block's P has been given, and the softmax does not wait for the
+// products (with one S of 128 keys it did for 1740 of 4400 clocks a block).
+// The ring of K and V runs on across items, a Q tile is loaded when the
+// previous item's last S is done, and the next item's first two S run under an
+// item's epilogue (a launch, load and epilogue of its own took 19% of an
+// item of 20 blocks).
 template <bool BF, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -329,24 +356,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sQ = smem;               // [2] query tiles, at the end O
+  uint8_t* sQ = smem;               // [2] query tiles
   uint8_t* sKV = sQ + 2 * kTile;    // stage st: K at +0, V at +kTile64
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kSt * 2 * kTile64);
+  uint8_t* sO = sKV + kSt * 2 * kTile64;  // a box per softmax warp
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sO + 8 * C::kBox);
   uint64_t* kv_full = bars;          // [4] stages
   uint64_t* kv_empty = bars + 4;     // [4]
   uint64_t* s_full = bars + 8;       // [tile][buffer]: S ready
   uint64_t* p_full = bars + 12;      // [tile][buffer]: P stored (and O rescaled)
   uint64_t* o_full = bars + 16;      // [tile][buffer]: the buffer's P V done
   uint64_t* q_full = bars + 20;      // [2] tiles
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 22);
+  uint64_t* q_empty = bars + 22;     // [2] tiles: the item's last S done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int npairs = ((a.sq + kBM - 1) / kBM + 1) / 2;
-  const int pair = npairs - 1 - static_cast<int>(blockIdx.y);  // longest rows first
-  const int head = blockIdx.x % a.heads, bi = blockIdx.x / a.heads;
-  const int kvh = head / a.group;
-  const int r0 = 2 * pair * kBM;
-  const BlockList<kB64> bl(r0, a);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
@@ -356,7 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i], 4);  // one arrival per warp of the tile's softmax group
       mbar_init(&o_full[i], 1);
     }
-    for (int i = 0; i < 2; ++i) mbar_init(&q_full[i], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -367,100 +393,118 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_slot);  // uniform
-  // Tile x, buffer b (the parity of the block's place in the list): S at
+  // Tile x, buffer b (the parity of the block's place in the ring): S at
   // columns [256 x + 64 b, + 64), P over its first 32; O at [256 x + 128, + DH).
   auto tS = [tmem](int x, int b) { return tmem + static_cast<uint32_t>(256 * x + 64 * b); };
   auto tO = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
+  bool ok = true;  // no wait of this thread has given up
 
   if (warp == 0) {
-    if (lane == 0 && bl.n > 0) {
+    if (lane == 0) {
       // ------------------------------------------------------- TMA producer
-      bool ok = true;
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmK);
       tma_prefetch_desc(&tmV);
       tma_prefetch_desc(&tmO);
-      auto load_q = [&](int x) {
-        mbar_arrive_expect_tx(&q_full[x], kTile);
-        load_tile<DH>(sQ + x * kTile, &tmQ, &q_full[x], head, r0 + x * kBM, bi, kBM);
-      };
-      load_q(0);
-      for (int j = 0; j < bl.n && ok; ++j) {
-        const int st = j % kSt;
-        const uint32_t ph = static_cast<uint32_t>(j / kSt) & 1u;
-        const int krow = bl.block(j) * kB64;
-        uint8_t* dst = sKV + st * (2 * kTile64);
-        if (!(ok = mbar_wait(&kv_empty[st], ph ^ 1u, a.status, kStatusAttnTimeout))) break;
-        mbar_arrive_expect_tx(&kv_full[st], 2 * kTile64);
-        load_tile<DH>(dst, &tmK, &kv_full[st], kvh, krow, bi, kB64);
-        load_tile<DH>(dst + kTile64, &tmV, &kv_full[st], kvh, krow, bi, kB64);
-        if (j == 0 && r0 + kBM < a.sq) load_q(1);
+      uint32_t g = 0u, nq[2] = {0u, 0u};  // blocks and query tiles loaded so far
+      for (int t = 0; ok; ++t) {
+        const FwdItem it(t, a);
+        if (it.r0 < 0) break;
+        const BlockList<kB64> bl(it.r0, a);
+        auto load_q = [&](int x) {
+          if (!it.has_q(x, bl.n, a)) return true;
+          if (!mbar_wait(&q_empty[x], (nq[x] & 1u) ^ 1u, a.status, kStatusAttnTimeout))
+            return false;
+          ++nq[x];
+          mbar_arrive_expect_tx(&q_full[x], kTile);
+          load_tile<DH>(sQ + x * kTile, &tmQ, &q_full[x], it.head, it.r0 + x * kBM, it.bi, kBM);
+          return true;
+        };
+        if (!(ok = load_q(0))) break;
+        for (int j = 0; j < bl.n; ++j, ++g) {
+          const int st = static_cast<int>(g % kSt);
+          uint8_t* dst = sKV + st * (2 * kTile64);
+          const int krow = bl.block(j) * kB64, kvh = it.head / a.group;
+          if (!(ok = mbar_wait(&kv_empty[st], ((g / kSt) & 1u) ^ 1u, a.status,
+                               kStatusAttnTimeout)))
+            break;
+          mbar_arrive_expect_tx(&kv_full[st], 2 * kTile64);
+          load_tile<DH>(dst, &tmK, &kv_full[st], kvh, krow, it.bi, kB64);
+          load_tile<DH>(dst + kTile64, &tmV, &kv_full[st], kvh, krow, it.bi, kB64);
+          if (j == 0 && !(ok = load_q(1))) break;
+        }
       }
     }
   } else if (warp <= 2) {
-    if (bl.n > 0) {
-      // -------------------------------------------------- MMA issuer of a tile
-      // Per listed block j that the tile sees: P V_j; then S of block j + 2, in
-      // the same buffer.  The MMAs run in issue order, so S overwrites P only
-      // after its product has read it.  An issuer of its own per tile: one for
-      // both was busy for 1.5 times as long as its products ran, most of it
-      // waiting for one tile while the other's P was there.
-      constexpr uint32_t kIdS = idesc<BF>(kBM, kB64, false, false);  // Q K^T
-      constexpr uint32_t kIdO = idesc<BF>(kBM, DH, false, true);     // P V
-      const int x = warp - 1;
-      const uint32_t q_addr = smem_u32(sQ + x * kTile);
-      uint32_t pbits = 0u;  // bit b: parity of p_full[x][b]'s next wait
-      bool some = false;    // a P V product has been issued
-      bool ok = bl.count(x) == 0 ||
-                warp_mbar_wait(&q_full[x], 0, a.status, kStatusAttnTimeout);
-      for (int j = -2; j < bl.n && ok; ++j) {
-        const int b = j & 1;
-        const int jn = j + 2, st = j & (kSt - 1), stn = jn & (kSt - 1);
+    // ---------------------------------------------------- MMA issuer of a tile
+    // Per listed block j that the tile sees: P V_j; then S of block j + 2, in
+    // the same buffer.  The MMAs run in issue order, so S overwrites P only
+    // after its product has read it.  An issuer of its own per tile: one for
+    // both was busy for 1.5 times as long as its products ran, most of it
+    // waiting for one tile while the other's P was there.
+    constexpr uint32_t kIdS = idesc<BF>(kBM, kB64, false, false);  // Q K^T
+    constexpr uint32_t kIdO = idesc<BF>(kBM, DH, false, true);     // P V
+    const int x = warp - 1;
+    const uint32_t q_addr = smem_u32(sQ + x * kTile);
+    uint32_t pbits = 0u;       // bit b: parity of p_full[x][b]'s next wait
+    uint32_t g0 = 0u, nq = 0u;  // blocks and query tiles of the items before
+    for (int t = 0; ok; ++t) {
+      const FwdItem it(t, a);
+      if (it.r0 < 0) break;
+      const BlockList<kB64> bl(it.r0, a);
+      const int total = bl.count(x);
+      bool some = false;  // a P V product of this item has been issued
+      int left = total;   // S products to issue
+      if (it.has_q(x, bl.n, a)) {
+        if (!(ok = warp_mbar_wait(&q_full[x], nq & 1u, a.status, kStatusAttnTimeout))) break;
+        ++nq;
+        if (total == 0) warp_umma_commit(&q_empty[x]);
+      }
+      for (int j = -2; j < bl.n; ++j) {
+        const uint32_t g = g0 + static_cast<uint32_t>(j), gn = g + 2u;
+        const int b = static_cast<int>(g & 1u);
         if (j >= 0 && bl.sees(x, j)) {
           if (!(ok = warp_mbar_wait(&p_full[2 * x + b], (pbits >> b) & 1u, a.status,
                                     kStatusAttnTimeout)))
             break;
           pbits ^= 1u << b;
           tc_fence_after();
-          const uint32_t v_addr = smem_u32(sKV + st * (2 * kTile64) + kTile64);
+          const uint32_t v_addr = smem_u32(sKV + (g % kSt) * (2 * kTile64) + kTile64);
           warp_umma_ts4(tO(x), tS(x, b), sw128_desc(v_addr, kB64 * 128, 1024), kIdO,
                         some ? 1u : 0u);
           warp_umma_commit(&o_full[2 * x + b]);
           some = true;
         }
-        if (j >= 0) warp_umma_commit(&kv_empty[st]);
-        if (jn < bl.n) {
+        if (j >= 0) warp_umma_commit(&kv_empty[g % kSt]);
+        if (j + 2 < bl.n) {
           // Waited for whether seen or not: an issuer that skipped blocks would
           // release a stage twice.
-          if (!(ok = warp_mbar_wait(&kv_full[stn], static_cast<uint32_t>(jn / kSt) & 1u, a.status,
+          if (!(ok = warp_mbar_wait(&kv_full[gn % kSt], (gn / kSt) & 1u, a.status,
                                     kStatusAttnTimeout)))
             break;
-          if (bl.sees(x, jn)) {
+          if (bl.sees(x, j + 2)) {
             tc_fence_after();
-            const uint32_t k_addr = smem_u32(sKV + stn * (2 * kTile64));
+            const uint32_t k_addr = smem_u32(sKV + (gn % kSt) * (2 * kTile64));
 #pragma unroll
             for (int c = 0; c < DH / 64; ++c)
               warp_umma_ss4(tS(x, b), sw128_desc(q_addr + c * kBM * 128, 16, 1024),
                             sw128_desc(k_addr + c * kB64 * 128, 16, 1024), kIdS, c > 0 ? 1u : 0u);
             warp_umma_commit(&s_full[2 * x + b]);
+            if (--left == 0) warp_umma_commit(&q_empty[x]);
           }
         }
       }
+      g0 += static_cast<uint32_t>(bl.n);
     }
   } else if (warp >= 4) {
     // ----------------------------------------------------------- softmax
     const int x = (warp - 4) >> 2;
     const int quarter = warp & 3;
-    const int row0 = r0 + x * kBM + quarter * 32, r = row0 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t orow_t = tO(x) + lane_off;
-    // Rows past the end take the last position: their results are not stored.
-    const int p = min(r, a.sq - 1) + a.off;
-    const int total = bl.count(x);
-    float m_used = -INFINITY, l_run = 0.0f;
-    bool ok = true;
-    int cnt = 0, last = 0;   // blocks so far; the buffer of the last one
-    uint32_t bits = 0u;      // bit b: parity of s_full[x][b]'s next wait
+    uint8_t* box = sO + (warp - 4) * C::kBox;
+    uint32_t bits = 0u;  // bit b: parity of s_full[x][b]'s next wait
+    uint32_t g0 = 0u;    // blocks of the items before
     // The buffer's P V, by the parity its S had.
     auto wait_o = [&](int b) {
       const bool done = mbar_wait(&o_full[2 * x + b], ((bits >> b) & 1u) ^ 1u, a.status,
@@ -468,109 +512,117 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (done) tc_fence_after();
       return done;
     };
-    for (int j = 0; j < bl.n && cnt < total; ++j) {
-      if (!bl.sees(x, j)) continue;
-      const int b = j & 1;
-      const uint32_t srow = tS(x, b) + lane_off;
-      if (!(ok = mbar_wait(&s_full[2 * x + b], (bits >> b) & 1u, a.status, kStatusAttnTimeout)))
-        break;
-      bits ^= 1u << b;
-      tc_fence_after();
-      const int k0 = bl.block(j) * kB64;
-      const RowMask mask = row_mask(p, k0, a);
-      const bool all = all_visible(r0 + x * kBM + a.off, k0, a);
-      // A warp none of whose rows has seen a key yet takes the exact maximum.
-      const bool first = __all_sync(0xffffffffu, m_used == -INFINITY);
-      if (first) m_used = row_max_masked(srow, mask) * a.scale_log2;
-      uint32_t pk[kB64 / 2];
-      // A row that has seen no key yet (m_used = -inf) has P = 0 by the mask;
-      // 0 stands in for its maximum.
-      float rs = all ? exp_row<BF, true>(srow, mask, a.scale_log2,
-                                         m_used == -INFINITY ? 0.0f : m_used, pk)
-                     : exp_row<BF, false>(srow, mask, a.scale_log2,
-                                          m_used == -INFINITY ? 0.0f : m_used, pk);
-      // The first block set the maximum in use, so its P <= 1.  Later blocks:
-      // a row sum above kCheckSum, or a row without a maximum so far, sends
-      // the warp to the exact maximum.
-      if (!first && __any_sync(0xffffffffu, rs > kCheckSum || m_used == -INFINITY)) {
-        const float m_new = row_max_masked(srow, mask) * a.scale_log2;
-        const bool need = m_new > m_used + kRescaleLog2;
-        if (__any_sync(0xffffffffu, need)) {
-          // Recompute P at the new maximum (S is intact: P has not been
-          // stored) and rescale O, once the previous P V is done, and l.
-          // From -inf the factor is 0, on sums that are 0.
-          const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
-          if (need) m_used = m_new;
-          rs = exp_row<BF, false>(srow, mask, a.scale_log2,
-                                  m_used == -INFINITY ? 0.0f : m_used, pk);
-          if (!(ok = last == b ? true : wait_o(last))) break;
+    for (int t = 0; ok; ++t) {
+      const FwdItem it(t, a);
+      if (it.r0 < 0) break;
+      const BlockList<kB64> bl(it.r0, a);
+      const int row0 = it.r0 + x * kBM + quarter * 32, r = row0 + lane;
+      // Rows past the end take the last position: their results are not stored.
+      const int p = min(r, a.sq - 1) + a.off;
+      const int total = bl.count(x);
+      float m_used = -INFINITY, l_run = 0.0f;
+      int cnt = 0, last = 0;  // blocks so far; the buffer of the last one
+      for (int j = 0; j < bl.n && cnt < total; ++j) {
+        if (!bl.sees(x, j)) continue;
+        const int b = static_cast<int>((g0 + j) & 1u);
+        const uint32_t srow = tS(x, b) + lane_off;
+        if (!(ok = mbar_wait(&s_full[2 * x + b], (bits >> b) & 1u, a.status, kStatusAttnTimeout)))
+          break;
+        bits ^= 1u << b;
+        tc_fence_after();
+        const int k0 = bl.block(j) * kB64;
+        const RowMask mask = row_mask(p, k0, a);
+        const bool all = all_visible(it.r0 + x * kBM + a.off, k0, a);
+        // A warp none of whose rows has seen a key yet takes the exact maximum.
+        const bool first = __all_sync(0xffffffffu, m_used == -INFINITY);
+        if (first) m_used = row_max_masked(srow, mask) * a.scale_log2;
+        uint32_t pk[kB64 / 2];
+        // A row that has seen no key yet (m_used = -inf) has P = 0 by the mask;
+        // 0 stands in for its maximum.
+        float rs = all ? exp_row<BF, true>(srow, mask, a.scale_log2,
+                                           m_used == -INFINITY ? 0.0f : m_used, pk)
+                       : exp_row<BF, false>(srow, mask, a.scale_log2,
+                                            m_used == -INFINITY ? 0.0f : m_used, pk);
+        // The first block set the maximum in use, so its P <= 1.  Later blocks:
+        // a row sum above kCheckSum, or a row without a maximum so far, sends
+        // the warp to the exact maximum.
+        if (!first && __any_sync(0xffffffffu, rs > kCheckSum || m_used == -INFINITY)) {
+          const float m_new = row_max_masked(srow, mask) * a.scale_log2;
+          const bool need = m_new > m_used + kRescaleLog2;
+          if (__any_sync(0xffffffffu, need)) {
+            // Recompute P at the new maximum (S is intact: P has not been
+            // stored) and rescale O, once the previous P V is done, and l.
+            // From -inf the factor is 0, on sums that are 0.
+            const float alpha = need ? ex2_approx(m_used - m_new) : 1.0f;
+            if (need) m_used = m_new;
+            rs = exp_row<BF, false>(srow, mask, a.scale_log2,
+                                    m_used == -INFINITY ? 0.0f : m_used, pk);
+            if (!(ok = last == b ? true : wait_o(last))) break;
 #pragma unroll 1
-          for (int c = 0; c < DH; c += 32) {
-            float o[32];
-            tmem_ld32(orow_t + c, o);
+            for (int c = 0; c < DH; c += 32) {
+              float o[32];
+              tmem_ld32(orow_t + c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(orow_t + c, o);
+              for (int i = 0; i < 32; ++i) o[i] *= alpha;
+              tmem_st32(orow_t + c, o);
+            }
+            l_run *= alpha;
           }
-          l_run *= alpha;
         }
-      }
-      l_run += rs;
+        l_run += rs;
 #pragma unroll
-      for (int c = 0; c < kB64 / 2; c += 16) {
-        uint32_t q16[16];
+        for (int c = 0; c < kB64 / 2; c += 16) {
+          uint32_t q16[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q16[i] = pk[c + i];
-        tmem_st16(srow + c, q16);
+          for (int i = 0; i < 16; ++i) q16[i] = pk[c + i];
+          tmem_st16(srow + c, q16);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
+        last = b;
+        ++cnt;
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[2 * x + b]);
-      last = b;
-      ++cnt;
-    }
-    if (ok && total > 0) ok = wait_o(last);
-    if (ok && total == 0 && bl.n > 0 && r0 + x * kBM < a.sq)
-      ok = mbar_wait(&q_full[x], 0, a.status, kStatusAttnTimeout);
-    if (ok) {
-      // O through the warp's rows of the query tile, which has landed and been
-      // read by every product by now.
+      if (ok && total > 0) ok = wait_o(last);
+      if (!ok) break;
+      g0 += static_cast<uint32_t>(bl.n);
       const bool some = l_run > 0.0f;
       const float inv = some ? 1.0f / l_run : 0.0f;
-      uint8_t* box = sQ + x * kTile + quarter * 32 * 128;
+#pragma unroll 1
+      for (int h = 0; h < DH / 64; ++h) {
+        if (lane == 0) bulk_wait_read<0>();  // the box's last store has read it
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < DH; c += 32) {
-        float v[32];
-        if (total > 0) tmem_ld32(orow_t + c, v);
-        if (!some) {
+        for (int c = 0; c < 64; c += 32) {
+          float v[32];
+          if (total > 0) tmem_ld32(orow_t + 64 * h + c, v);
+          if (!some) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(box + lane * 128 + (((c / 8 + q) ^ (lane & 7)) << 4)) =
+                pack8t<BF>(v + 8 * q, inv);
         }
-        uint8_t* dst = box + (c >> 6) * kBM * 128 + lane * 128;
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(dst + ((((c & 63) / 8 + q) ^ (lane & 7)) << 4)) =
-              pack8t<BF>(v + 8 * q, inv);
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0 && row0 < a.sq) {
-#pragma unroll
-        for (int c = 0; c < DH / 64; ++c)
-          tma_store_3d(&tmO, box + c * kBM * 128, head * DH + 64 * c, row0, bi);
-        bulk_commit();
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < a.sq) {
+          tma_store_3d(&tmO, box, it.head * DH + 64 * h, row0, it.bi);
+          bulk_commit();
+        }
       }
       if (r < a.sq)
-        a.lse[(static_cast<long long>(bi) * a.heads + head) * a.sq + r] =
+        a.lse[(static_cast<long long>(it.bi) * a.heads + it.head) * a.sq + r] =
             some ? (m_used + log2f(l_run)) * kLn2 : -INFINITY;
-      if (lane == 0) bulk_wait_read<0>();
     }
+    if (lane == 0) bulk_wait_read<0>();
   }
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  leave(!ok);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
@@ -715,10 +767,10 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   auto tS = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x); };
   auto tP = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 64); };
   auto tQ = [tmem](int x) { return tmem + static_cast<uint32_t>(256 * x + 128); };
+  bool ok = true;  // no wait of this thread has given up
 
   if (warp == 0) {
     if (lane == 0 && bl.n > 0) {
-      bool ok = true;
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmdO);
       tma_prefetch_desc(&tmK);
@@ -759,7 +811,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
       };
       const int total[2] = {bl.count(0), bl.count(1)};
       int done[2] = {0, 0};
-      bool ok = warp_mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
+      ok = warp_mbar_wait(qd_full, 0, a.status, kStatusAttnTimeout);
       auto issue = [&](auto two) {
         for (int j = -1; j < bl.n && ok; ++j) {
           const bool more = j + 1 < bl.n;
@@ -811,7 +863,6 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
     const float2 nl2 = make_float2(nl, nl), nd2 = make_float2(ndd, ndd);
     const int p = rc + a.off;
     const int total = bl.count(x);
-    bool ok = true;
     // One loop for tiles that give dS in two terms, one for the others.
     auto blocks = [&](auto two) {
       int cnt = 0;
@@ -901,7 +952,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
   }
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  leave(!ok);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
@@ -1050,6 +1101,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
   auto tS = [tmem](int st) { return tmem + static_cast<uint32_t>(64 * st); };
   auto tP = [tmem](int st) { return tmem + static_cast<uint32_t>(128 + 64 * st); };
   const uint32_t tdV = tmem + 256, tdK = tmem + 384;
+  bool ok = true;  // no wait of this thread has given up
 
   if (warp == 0) {
     if (lane == 0) {
@@ -1057,7 +1109,6 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
       tma_prefetch_desc(&tmV);
       tma_prefetch_desc(&tmQ);
       tma_prefetch_desc(&tmdO);
-      bool ok = true;
       long long g = 0;  // query blocks loaded so far: the ring position
       uint32_t it_no = 0;  // items with queries so far
       for (int r = 0; ok; ++r) {
@@ -1120,7 +1171,6 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
         warp_umma_commit(&s_full[st]);
         return true;
       };
-      bool ok = true;
       long long g = 0;  // query blocks of the items before this one
       uint32_t it_no = 0;
       for (int r = 0; ok; ++r) {
@@ -1181,7 +1231,6 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
     const int r = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
-    bool ok = true;
     long long gb = 0;  // query blocks of the items before this one
     uint32_t it_no = 0;
     for (int ri = 0; ok; ++ri) {
@@ -1326,7 +1375,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
 
   __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  leave(!ok);
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
@@ -1516,7 +1565,9 @@ tp_status fwd(const WindowAttn& w, cudaStream_t stream) {
   if (tp_status s = smem_opt_in(window_fwd<BF, DH>, smem, "window attention smem"); s != TP_OK)
     return s;
   const int64_t npairs = ((w.sq + kBM - 1) / kBM + 1) / 2;
-  dim3 grid(static_cast<unsigned>(w.b * w.heads), static_cast<unsigned>(npairs));
+  a.bkv = static_cast<int>(w.b * w.kv_heads);
+  a.items = static_cast<int>(npairs * w.b * w.heads);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(a.items, sm_count()));
   {
     LaunchScope scope(TP_KIND_ATTN_FWD, 4.0 * DH * visible_pairs(w),
                       4.0 * double(w.b) * (w.sq * nq + w.sk * nk), stream);
