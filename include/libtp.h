@@ -21,7 +21,8 @@
  * - Every pointer is a DEVICE pointer owned by the caller; the library keeps
  *   no reference after the call returns and allocates no device memory.
  *   Scratch space comes from the caller's workspace `ws` of `ws_bytes`
- *   bytes, sized with tp_workspace_size().
+ *   bytes, sized with tp_workspace_size().  Calls that may run at the same
+ *   time need workspaces of their own.
  * - Each call validates its arguments on the host, synchronously, before any
  *   launch, and then enqueues its kernels on `stream` (a cudaStream_t; NULL is
  *   the legacy default stream) and returns without waiting.
@@ -418,6 +419,8 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
  *   larger batches'.
+ *   ws: tp_workspace_size(TP_OP_GLU_FWD, M, h, f, 0, t, TP_BF16); what serves M
+ *   tokens also serves fewer.
  * Errors: NULL X / Wgu / Wd / Z; f % t; alignment (h, f multiples of 8);
  *   dtype must be TP_BF16 (else TP_ERR_UNSUPPORTED); act unknown
  *   (TP_ERR_UNSUPPORTED); TP_ERR_WORKSPACE.
@@ -552,7 +555,8 @@ size_t tp_window_attn_workspace_size(int64_t b, int64_t sq, int64_t sk, int head
  *   lens [b] int32 on the device (values outside [0, cap] are clamped to it);
  *   lens[i] == 0: O 0, LSE -inf.  Keys at and past lens[i] are not read.
  *   LSE [b, heads] fp32 or NULL.
- *   ws: tp_window_decode_workspace_size() bytes.
+ *   ws: tp_window_decode_workspace_size() bytes; what serves a batch also
+ *   serves smaller ones.
  * Errors: as tp_window_attn_fwd, plus TP_ERR_WORKSPACE.
  */
 tp_status tp_window_attn_decode(const void* Q, int64_t ldq, const void* K, int64_t ldk,

@@ -893,8 +893,11 @@ tp_status vocab_ce_bwd(const void* X, const void* E, const int32_t* targets, con
 
 // ------------------------------------------------ gated feed-forward block
 
-// H, in two terms for the fewest tokens.
-size_t glu_h_bytes(int64_t M, int64_t f) { return M * f * 2 * (M <= kThinTwoTermM ? 2 : 1); }
+// H, in two terms for the fewest tokens; never less than for fewer tokens, so
+// a workspace for a batch serves smaller ones.
+size_t glu_h_bytes(int64_t M, int64_t f) {
+  return (M <= kThinTwoTermM ? 2 * M : std::max(M, 2 * kThinTwoTermM)) * f * 2;
+}
 
 size_t glu_fwd_ws_min(int64_t M, int64_t f) { return align_up(glu_h_bytes(M, f), 256) + 256; }
 

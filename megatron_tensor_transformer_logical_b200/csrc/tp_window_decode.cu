@@ -471,12 +471,17 @@ tp_status decode(const WindowDecode& w, void* scratch, cudaStream_t stream) {
 
 }  // namespace
 
+// Enough for this batch and every smaller one: n items are cut into fewer than
+// 2 SMs + n slices, and into none from 2 SMs on.
 size_t window_decode_scratch_bytes(const WindowDecode& w) {
-  const int splits = plan_splits(w);
-  if (splits == 1) return 256;
+  const int64_t keys = std::min(w.cap, w.window + w.sinks);
+  const int64_t most = std::min<int64_t>((keys + kMinKeys - 1) / kMinKeys, kMaxSplits);
+  if (most == 1) return 256;
   const int group = w.heads / w.kv_heads;
-  const size_t rows = static_cast<size_t>(w.b) * w.kv_heads * ((group + kRows - 1) / kRows) *
-                      splits * std::min(group, kRows);
+  const int64_t full = 2LL * sm_count();
+  const int64_t n = std::min<int64_t>(full, w.b * w.kv_heads * ((group + kRows - 1) / kRows));
+  const size_t rows =
+      static_cast<size_t>(std::min(full + n - 1, n * most)) * std::min(group, kRows);
   return align256(rows * sizeof(float2)) + align256(rows * w.d * sizeof(float));
 }
 

@@ -55,3 +55,10 @@ def test_workspace_sizes(lib):
     assert ws(L.TP_OP_GLU_FWD, 100, 128, 0) == 0
     assert ws(L.TP_OP_GLU_FWD, 100, 128, 512, L.TP_F32) == 0
     assert ws(L.TP_OP_GLU_BWD, 100, 128, 1 << 40) == 0
+
+
+def test_a_forward_workspace_serves_fewer_tokens(lib):
+    for f in (8, 2816, 14336):
+        sizes = [lib.tp_workspace_size(L.TP_OP_GLU_FWD, M, 1024, f, 0, 1, L.TP_BF16)
+                 for M in range(1, 70)]
+        assert sizes == sorted(sizes)

@@ -84,3 +84,19 @@ def test_workspace_sizes(lib):
                                (64, 4096, 32, 8, 512, 128), (1, 8192, 8, 8, 8192, 0)):
         stats = 2 * (b * h * s + 64) * 4 + 512
         assert ws(b, s, s, h, kv, 128, w, sk) - stats <= 8 * 160 * 2 * 128 * 128 * 4
+
+
+@pytest.mark.parametrize("heads,kv,cap,window,sinks", [
+    (32, 8, 8192, 4096, 4), (32, 4, 131072, 131072, 0), (40, 1, 3000, 700, 3), (8, 8, 300, 300, 0)])
+def test_a_decode_workspace_serves_smaller_batches(lib, heads, kv, cap, window, sinks):
+    size = lambda b: lib.tp_window_decode_workspace_size(b, cap, heads, kv, 128, window, sinks)
+    sizes = [size(b) for b in range(1, 400)]
+    assert sizes == sorted(sizes)
+    # what the launch lays out: a slice per 256 keys at most, enough of them for
+    # two blocks per SM (148 of them; without a GPU the library plans for as many)
+    group = heads // kv
+    for b, have in zip(range(1, 400), sizes):
+        items, keys = b * kv * -(-group // 16), min(cap, window + sinks)
+        splits = max(1, min(-(-2 * 148 // items), -(-keys // 256), 255))
+        rows = items * splits * min(group, 16) if splits > 1 else 0
+        assert have >= -(-rows * 8 // 256) * 256 + rows * 128 * 4
