@@ -58,7 +58,12 @@ def reference(Q, K, V, b, heads, kv, window, sinks, scale, dO=None):
             l = torch.logsumexp(s, 1)
             P = torch.where(seen, torch.exp(s - l[:, None]), torch.zeros_like(s))
             O = P @ v
+            # Below 2^-14 an fp16 P is off by up to 2^-25, half its smallest step, not
+            # by hs of itself; the row sum it is divided by is at least 1, since the
+            # maximum in use is that of keys the row has seen.  So the seen keys add
+            # 2^-25 |V| each (tiny / 2), which shows where sharp rows make O small.
             eO = hs * (P @ v.abs()) + hs * O.abs() + F32 * (P @ v.abs()) + tiny
+            eO = eO + tiny / 2 * (seen.double() @ v.abs())
             o["O"][i, :, h], t["O"][i, :, h] = O, eO
             lse[i, h] = l
             tl[i, h] = 2.0 ** -20 * (1 + (q.abs() @ k.abs().t()).amax(1) * scale)
@@ -396,3 +401,27 @@ def test_binding_refuses_mismatched_tensors():
         L.tp_window_attn_decode(Q[:2], K[:2].reshape(2, 1, 64), V[:2].reshape(2, 1, 64), lens,
                                 O[:2], None, 2, 1, 4, 0, torch.empty(256, dtype=torch.uint8,
                                                                     device="cuda"))
+
+
+@pytest.mark.parametrize("case,std", [
+    ((7, 300, 170, 32, 4, 128, 40, 2, BF), 1.0),    # first 130 queries see nothing
+    ((6, 333, 333, 40, 8, 64, 100, 3, FP), 6.0),    # late maxima
+    ((3, 600, 130, 64, 8, 64, 500, 0, BF), 1.0),    # a whole tile sees nothing
+    ((40, 130, 130, 16, 16, 128, 7, 0, BF), 6.0)],
+    ids=lambda c: str(c[0]) if isinstance(c, tuple) else None)
+def test_several_items_per_block(case, std):
+    """More (sequence, head, query tiles) than SMs, so every block takes several,
+    into columns and rows of a larger buffer that stays as it was around them."""
+    b, sq, sk, heads, kv, d, window, sinks, dt = case
+    Q, K, V, dO = make(b, sq, sk, heads, kv, d, dt, seed=5, std=std)
+    out = run(Q, K, V, dO, b, heads, kv, window, sinks)
+    ref, tol = reference(Q, K, V, b, heads, kv, window, sinks, d ** -0.5, dO)
+    for n in out:
+        close(out[n], ref[n], tol[n], n)
+    big = torch.full((b * sq + 5, heads * d + 72), 7.0, dtype=dt, device="cuda")
+    view = big[2:2 + b * sq, 64:64 + heads * d]
+    LSE = torch.empty(b, heads, sq, device="cuda")
+    L.tp_window_attn_fwd(Q, K, V, view, LSE, b, heads, kv, window, sinks)
+    assert torch.equal(view, out["O"]) and torch.equal(LSE, out["LSE"])
+    view.fill_(7.0)
+    assert bool((big == 7.0).all())
