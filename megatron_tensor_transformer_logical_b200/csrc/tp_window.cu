@@ -148,14 +148,14 @@ __device__ __forceinline__ Blocks blocks_of(int r0, const WinArgs& a) {
 
 // The CTA's list of key blocks for its two query tiles: [lo, hi], then sink
 // blocks [0, ns).  Every listed block is seen by one of the tiles at least.
-// With keys in front of the window, [lo, hi] runs from the diagonal down: each
-// row then meets visible keys, itself among them, in its tile's first block,
-// where the first block of the window may hide all of its keys from the last
-// rows and send them through the exact maximum a block later (187 against 194
-// us on 8192 tokens, 32 heads, window 1024, 4 sinks).  Without, it runs up
-// from block 0, where every row sees keys and the two tiles end a block apart,
-// so that one tile's epilogue overlaps the other's last block (68 against 76
-// us on 4096 tokens, 16 heads, all visible).
+// With keys in front of the window, [lo, hi] runs from the diagonal down: the
+// first keys that a row meets are its nearest ones, where the first block of
+// the window may hide all of its keys from the last rows and send them through
+// the exact maximum a block later (160 against 166 us on 8192 tokens, 32
+// heads, window 1024, 4 sinks; 23 against 21 on windows of 257, five blocks
+// long).  Without, it runs up from block 0, where every row sees keys and the
+// two tiles end apart, so that one tile's epilogue overlaps the other's last
+// blocks (73 against 81 us on 4096 tokens, 16 heads, all visible).
 template <int BN>
 struct BlockList {
   Blocks t0, t1;
@@ -249,9 +249,8 @@ __device__ __forceinline__ float row_max_masked(uint32_t srow, const RowMask& m)
 // the row sum of the unrounded P.  ALL: every row of the tile sees the whole
 // block.  Otherwise hidden keys give 0, and a chunk that no row of the warp
 // sees costs no exponential.  (Leaving the columns behind the sinks out of a
-// sink block's products as well was slower, 196 against 188 us on the case
-// above: the issuing thread's branches cost more than the narrow products
-// save.)
+// sink block's products as well was slower in a version with blocks of 128
+// keys, 196 against 188 us on the first case above.)
 template <bool BF, bool ALL>
 __device__ __forceinline__ float exp_row(uint32_t srow, const RowMask& mask, float scale_log2,
                                          float m, uint32_t (&pk)[kB64 / 2]) {
@@ -346,6 +345,11 @@ struct FwdItem {
 // previous item's last S is done, and the next item's first two S run under an
 // item's epilogue (a launch, load and epilogue of its own took 19% of an
 // item of 20 blocks).
+// Bound by the tensor pipe: a tile's block of 64 keys takes it 384 clocks for S
+// (both operands from shared memory, 6 KB per product of 32 clocks) and 256
+// for P V, 1280 for both tiles, and a pair of blocks takes 1550.  Measured:
+// 8192 tokens, 32 heads of 128, window 1024, 4 sinks (129 GFLOP) 160 us, 806
+// TFLOP/s; tensor pipe 47% of the cycles, exponentials 42%.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -707,7 +711,10 @@ struct DqSmem {
 
 // dQ: one CTA per (sequence, head, pair of query tiles), 64-key blocks; `cta`
 // counts them, heads fastest, longest rows first.  Per block and tile: S = Q
-// K^T, dP = dO V^T -> dS over S -> dQ += dS K.
+// K^T, dP = dO V^T -> dS over S -> dQ += dS K.  The tensor pipe takes 1024
+// clocks of a tile's block (S and dP, operands from shared memory, 768; dQ 256),
+// and one warp issues both tiles' products in turn: an issuer per tile, as in
+// the forward, was slower (767 against 747 us on the case below).
 template <bool BF, int DH>
 __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap& tmdO,
                                        const CUtensorMap& tmK, const CUtensorMap& tmV, int cta,
@@ -1045,6 +1052,12 @@ __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
 // previous item's last S^T / dP^T are done (kv_empty), and its first dV, dK
 // products wait until the previous epilogue has read the accumulators
 // (acc_empty).  Items without queries only write zeros.
+// The tensor pipe takes 1280 clocks of a block of 64 queries, a block 2300: the
+// element-wise warps take about 1650 of them from S^T to P^T (their row terms
+// wait for a shared memory that the products keep busy; reading them ahead,
+// which needs 64 registers more, did not pay).  Both parts on two sequences of
+// 4096, 32 + 8 heads of 128, window 1024, 4 sinks (301 GFLOP): 560 us, 540
+// TFLOP/s; with the products issued under a branch to one lane 630-676 us.
 template <bool BF, int DH>
 __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                          const CUtensorMap& tmQ, const CUtensorMap& tmdO,
