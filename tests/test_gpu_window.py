@@ -425,3 +425,24 @@ def test_several_items_per_block(case, std):
     assert torch.equal(view, out["O"]) and torch.equal(LSE, out["LSE"])
     view.fill_(7.0)
     assert bool((big == 7.0).all())
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_decode_of_few_outputs_rounds_once(dt):
+    """Up to 8192 outputs P has two terms, so O is off by its own rounding and the
+    fp32 parts of `reference` (2 hs^2 of P |V| is what two terms leave; for fp16
+    half its smallest step per key)."""
+    b, cap, heads, kv, d = 2, 700, 8, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(12)
+    Q, K, V = rn(g, b, heads * d, dt=dt), rn(g, b, cap, kv * d, dt=dt), rn(g, b, cap, kv * d, dt=dt)
+    lens = torch.full((b,), cap, dtype=torch.int32, device="cuda")
+    O, ws = torch.empty_like(Q), L.window_attn_decode_workspace(b, cap, heads, kv, d, 400, 3)
+    L.tp_window_attn_decode(Q, K, V, lens, O, None, heads, kv, 400, 3, ws)
+    ref, _ = reference(Q, K.reshape(b * cap, -1), V.reshape(b * cap, -1), b, heads, kv, 400, 3,
+                       d ** -0.5)
+    big, _ = reference(Q, K.reshape(b * cap, -1), V.abs().reshape(b * cap, -1), b, heads, kv, 400,
+                       3, d ** -0.5)
+    hs = half_step(dt)
+    tiny = 403 * 2.0 ** -25 * V.abs().max().double() if dt == FP else 0.0
+    tol = hs * ref["O"].abs() + (F32 + 2 * hs * hs) * big["O"] + tiny
+    close(O, ref["O"], tol, "O")
