@@ -1307,22 +1307,31 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
             }
             tmem_st16(tS(st) + lane_off + c + 16, pl);
             tmem_st16(tP(st) + lane_off + c + 16, dl);
+          } else if (__all_sync(0xffffffffu, full)) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
+              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
+              const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+              const float2 g = __fmul2_rn(p, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd));
+              pk[i >> 1] = pack2<BF>(p.x, p.y);
+              dk[i >> 1] = pack2<BF>(g.x, g.y);
+            }
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
               const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
-              float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
               float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
-              if (!full) {
-                // hidden queries may stand on the row terms of another sequence
-                const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
-                p = make_float2(v0 ? p.x : 0.0f, v1 ? p.y : 0.0f);
-                d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
-              }
-              pk[i >> 1] = pack2<BF>(p.x, p.y);
+              // hidden queries may stand on the row terms of another sequence
+              const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
+              const float2 p =
+                  make_float2(v0 ? ex2_approx(t.x) : 0.0f, v1 ? ex2_approx(t.y) : 0.0f);
+              d = make_float2(v0 ? d.x : 0.0f, v1 ? d.y : 0.0f);
               const float2 g = __fmul2_rn(p, d);
+              pk[i >> 1] = pack2<BF>(p.x, p.y);
               dk[i >> 1] = pack2<BF>(g.x, g.y);
             }
           }
