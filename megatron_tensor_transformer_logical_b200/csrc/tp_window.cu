@@ -97,6 +97,11 @@ __device__ __forceinline__ void split2(float2 v, uint32_t& hi, uint32_t& lo) {
   lo = pack2<BF>(v.x - h.x, v.y - h.y);
 }
 
+// Values i and i + 1 of the four that hold them, i even.
+__device__ __forceinline__ float2 half4(const float4& v, int i) {
+  return (i & 2) ? make_float2(v.z, v.w) : make_float2(v.x, v.y);
+}
+
 // Eight fp32 values as one 16-byte store of the input type.
 template <bool BF>
 __device__ __forceinline__ uint4 pack8t(const float* v, float f) {
@@ -827,8 +832,8 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
           for (int x = 0; x < 2; ++x) {
             if (!ok) break;
             if (j >= 0 && bl.sees(x, j)) {
-              if (!(ok = warp_mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u, a.status,
-                                   kStatusAttnTimeout)))
+              if (!(ok = warp_mbar_wait(&ds_full[x], static_cast<uint32_t>(done[x]) & 1u,
+                                        a.status, kStatusAttnTimeout)))
                 break;
               tc_fence_after();
               const uint32_t k_addr = smem_u32(sKV + (j % kKvStages) * (2 * kTile64));
@@ -840,8 +845,9 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
             if (more && bl.sees(x, j + 1)) {
               if (!kv_next) {
                 const int ks = (j + 1) % kKvStages;
-                if (!(ok = warp_mbar_wait(&kv_full[ks], static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
-                                     a.status, kStatusAttnTimeout)))
+                if (!(ok = warp_mbar_wait(&kv_full[ks],
+                                          static_cast<uint32_t>((j + 1) / kKvStages) & 1u,
+                                          a.status, kStatusAttnTimeout)))
                   break;
                 tc_fence_after();
                 kv_next = true;
@@ -903,7 +909,7 @@ __device__ __forceinline__ void bwd_dq(const CUtensorMap& tmQ, const CUtensorMap
               split2<BF>(g, pk[i >> 1], lk[i >> 1]);
             }
             tmem_st16(tP(x) + lane_off + c / 2, lk);
-          } else if (vis == 0xffffffffu) {
+          } else if (__all_sync(0xffffffffu, vis == 0xffffffffu)) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl2);
@@ -1052,12 +1058,11 @@ __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
 // previous item's last S^T / dP^T are done (kv_empty), and its first dV, dK
 // products wait until the previous epilogue has read the accumulators
 // (acc_empty).  Items without queries only write zeros.
-// The tensor pipe takes 1280 clocks of a block of 64 queries, a block 2300: the
-// element-wise warps take about 1650 of them from S^T to P^T (their row terms
-// wait for a shared memory that the products keep busy; reading them ahead,
-// which needs 64 registers more, did not pay).  Both parts on two sequences of
-// 4096, 32 + 8 heads of 128, window 1024, 4 sinks (301 GFLOP): 560 us, 540
-// TFLOP/s; with the products issued under a branch to one lane 630-676 us.
+// The tensor pipe takes 1280 clocks of a block of 64 queries, a block about 2200: the
+// element-wise warps take about 1500 of them from S^T to P^T.  Both parts on two
+// sequences of 4096, 32 + 8 heads of 128, window 1024, 4 sinks (301 GFLOP): 527
+// us at 1.70 GHz, 571 TFLOP/s; with the products issued under a branch to one
+// lane 630-676 us.
 template <bool BF, int DH>
 __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorMap& tmV,
                                          const CUtensorMap& tmQ, const CUtensorMap& tmdO,
@@ -1267,16 +1272,23 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
           const int qs = static_cast<int>(gj % kQdStages);
           const int q0 = (it.i0 + qi) * kB64;
           if (++qi == it.n) qi = 0;
-          if (!(ok = mbar_wait(&s_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
-                               kStatusAttnTimeout)))
-            break;
           // The block's row terms were staged with its Q / dO; the stage cannot
-          // be refilled before this block's products are done.
+          // be refilled before this block's products are done.  -LSE is read
+          // before S is there: while products run they take all of shared
+          // memory's bandwidth (896k cycles for the launch on the case above,
+          // 918k without; -D as well would spill, 909k).
           if (!(ok = mbar_wait(&qd_full[qs], static_cast<uint32_t>(gj / kQdStages) & 1u, a.status,
                                kStatusAttnTimeout)))
             break;
+          const float4* wnl = reinterpret_cast<const float4*>(s_stat + qs * (2 * kB64) + c);
+          const float4* wnd = wnl + kB64 / 4;
+          float4 nl4[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) nl4[i] = wnl[i];
+          if (!(ok = mbar_wait(&s_full[st], static_cast<uint32_t>(gj >> 1) & 1u, a.status,
+                               kStatusAttnTimeout)))
+            break;
           tc_fence_after();
-          const float* wstat = s_stat + qs * (2 * kB64) + c;
           const int lo = qlo - q0 - c, hi = qhi - q0 - c;  // visible columns lo <= i < hi
           float sv[32], pv[32];
           tmem_ld32x2(tS(st) + lane_off + c, sv, tP(st) + lane_off + c, pv);
@@ -1294,8 +1306,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
             uint32_t pl[16], dl[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
-              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 nl = half4(nl4[i >> 2], i), nd = half4(wnd[i >> 2], i);
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
               float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
               const bool v0 = (vis >> i) & 1u, v1 = (vis >> (i + 1)) & 1u;
@@ -1310,8 +1321,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
           } else if (__all_sync(0xffffffffu, full)) {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
-              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 nl = half4(nl4[i >> 2], i), nd = half4(wnd[i >> 2], i);
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
               const float2 p = make_float2(ex2_approx(t.x), ex2_approx(t.y));
               const float2 g = __fmul2_rn(p, __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd));
@@ -1321,8 +1331,7 @@ __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorM
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 2) {
-              const float2 nl = *reinterpret_cast<const float2*>(wstat + i);
-              const float2 nd = *reinterpret_cast<const float2*>(wstat + kB64 + i);
+              const float2 nl = half4(nl4[i >> 2], i), nd = half4(wnd[i >> 2], i);
               const float2 t = __ffma2_rn(make_float2(sv[i], sv[i + 1]), sc2, nl);
               float2 d = __fadd2_rn(make_float2(pv[i], pv[i + 1]), nd);
               // hidden queries may stand on the row terms of another sequence
