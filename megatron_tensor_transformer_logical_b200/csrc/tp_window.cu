@@ -1060,8 +1060,8 @@ __device__ __forceinline__ int kv_item_index(int r, const WinArgs& a) {
 // (acc_empty).  Items without queries only write zeros.
 // The tensor pipe takes 1280 clocks of a block of 64 queries, a block about 2200: the
 // element-wise warps take about 1500 of them from S^T to P^T.  Both parts on two
-// sequences of 4096, 32 + 8 heads of 128, window 1024, 4 sinks (301 GFLOP): 527
-// us at 1.70 GHz, 571 TFLOP/s; with the products issued under a branch to one
+// sequences of 4096, 32 + 8 heads of 128, window 1024, 4 sinks (301 GFLOP): 520
+// us at 1.69 GHz, 579 TFLOP/s; with the products issued under a branch to one
 // lane 630-676 us.
 template <bool BF, int DH>
 __device__ __forceinline__ void bwd_dkdv(const CUtensorMap& tmK, const CUtensorMap& tmV,
