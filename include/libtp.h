@@ -554,6 +554,8 @@ size_t tp_window_attn_workspace_size(int64_t b, int64_t sq, int64_t sk, int head
  *   i * batch stride + c * row stride + g * d (elements), c < cap.
  *   lens [b] int32 on the device (values outside [0, cap] are clamped to it);
  *   lens[i] == 0: O 0, LSE -inf.  Keys at and past lens[i] are not read.
+ *   P enters P V in two terms (the rounded value and the rounded rest), so O is
+ *   off by its own rounding; a sequence's accuracy does not depend on its batch.
  *   LSE [b, heads] fp32 or NULL.
  *   ws: tp_window_decode_workspace_size() bytes; what serves a batch also
  *   serves smaller ones.

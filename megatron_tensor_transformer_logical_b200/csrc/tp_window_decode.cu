@@ -14,11 +14,13 @@
 //   cp.async stages (no block barrier in the loop) and keeps its own running
 //   maximum, sum and O; the block's warps are joined at its end.  Four stages
 //   or eight warps, which leave one block per SM, were 10-25% slower.
-// P is rounded to the type for P V, or, up to 8192 output values, given as the
-// rounded value and the rounded rest: few outputs do not average, and O is then
-// off by its own rounding alone instead of 1.4 times that.  For one sequence
-// over 131072 keys that is free (48.9 us both ways); for 32 of 4100 keys it
-// would cost 5% (92.5 against 87.6 us).
+// P enters P V as the rounded value and the rounded rest, so O is off by its
+// own rounding alone (with one term 1.4 times that), whatever else is in the
+// batch.  Groups of up to 8 query heads leave the rows 8-15 of the product
+// empty: the rests go there and cost no product of their own (32 sequences of
+// 4100 visible keys, 8 key heads of 128 read by 4 heads each: 85.6 us; with one
+// term and the empty rows computed 87.4).  Larger groups take a second one (16
+// such sequences, groups of 16: 69.2 against 65.0 us with one term).
 // Keys past the visible range are read as zeros and masked, so what the
 // cache holds beyond lens never enters, whatever it is.
 #include <cuda_bf16.h>
@@ -38,7 +40,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRows = 16;      // query heads per block
 constexpr int kMaxSplits = 255;
-constexpr int64_t kTwoTermOutputs = 8192;  // output values up to which P has two terms
+constexpr int kFoldRows = 8;   // query heads up to which the rests of P take the rows 8-15
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -152,11 +154,14 @@ __device__ __forceinline__ int slice_keys(int total, int splits) {
   return (per + step - 1) / step * step;
 }
 
-template <bool BF, int DH, int TERMS>
+// FOLD: at most kFoldRows query heads, row r + 8 of P holds the rest of row r.
+template <bool BF, int DH, bool FOLD>
 __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int kStageBytes = DecSmem<DH>::kStageBytes;
   constexpr int kRowBytes = DH * 2, kChunks = DH / 8;
+  constexpr int kTerms = FOLD ? 1 : 2;   // products of P V
+  constexpr int kHalves = FOLD ? 1 : 2;  // row halves that are query heads
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.x, split = blockIdx.y;
   const int gt = item % a.gtiles;
@@ -180,7 +185,7 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int row = r + 8 * (i & 1), col = 16 * kk + c + 8 * (i >> 1);
-        qf[kk][i] = row < rows ? *reinterpret_cast<const uint32_t*>(q + row * DH + col) : 0u;
+        qf[kk][i] = (i & 1) < kHalves && row < rows ? *reinterpret_cast<const uint32_t*>(q + row * DH + col) : 0u;
       }
   }
 
@@ -214,7 +219,12 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
   for (int n = 0; n < DH / 8; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[n][i] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+  float m[kHalves], l[kHalves];
+#pragma unroll
+  for (int h = 0; h < kHalves; ++h) {
+    m[h] = -INFINITY;
+    l[h] = 0.0f;
+  }
 
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
@@ -248,58 +258,58 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
     }
     // keys of this lane: t + 8 n + 2 (lane % 4) + {0, 1}
     const int t = first + i * kStep + 2 * (lane & 3);
-    float mx[2] = {-INFINITY, -INFINITY};
+    float mx[kHalves];
+    bool up = false;
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int h = 0; h < kHalves; ++h) {
+      mx[h] = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = t + 8 * n + (e & 1) < t1;
-        s[n][e] = in ? s[n][e] * a.scale_log2 : -INFINITY;
-        mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-      }
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+        for (int e = 2 * h; e < 2 * h + 2; ++e) {
+          const bool in = t + 8 * n + (e & 1) < t1;
+          s[n][e] = in ? s[n][e] * a.scale_log2 : -INFINITY;
+          mx[h] = fmaxf(mx[h], s[n][e]);
+        }
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      up = up || mx[h] > m[h];
     }
     // A tile holds at least one key, so after the first the maxima are finite
     // (for finite scores); O is rescaled only when one has risen.
-    if (__any_sync(0xffffffffu, mx[0] > m[0] || mx[1] > m[1])) {
+    if (__any_sync(0xffffffffu, up)) {
+      float f[kHalves];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kHalves; ++h) {
         const float mn = fmaxf(m[h], mx[h]);
-        const float f = m[h] == -INFINITY ? 0.0f : ex2_approx(m[h] - mn);
+        f[h] = m[h] == -INFINITY ? 0.0f : ex2_approx(m[h] - mn);
         m[h] = mn;
-        l[h] *= f;
-#pragma unroll
-        for (int n = 0; n < DH / 8; ++n) {
-          o[n][2 * h] *= f;
-          o[n][2 * h + 1] *= f;
-        }
+        l[h] *= f[h];
       }
+#pragma unroll
+      for (int n = 0; n < DH / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] *= f[(e >> 1) & (kHalves - 1)];
     }
-    uint32_t pf[TERMS][4];
+    uint32_t pf[kTerms][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[n][e] = ex2_approx(s[n][e] - m[e >> 1]);
-        l[e >> 1] += s[n][e];
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if constexpr (TERMS == 2)
-          split2<BF>(s[n][2 * h], s[n][2 * h + 1], pf[0][2 * n + h], pf[1][2 * n + h]);
+      for (int h = 0; h < kHalves; ++h) {
+        const float p0 = ex2_approx(s[n][2 * h] - m[h]), p1 = ex2_approx(s[n][2 * h + 1] - m[h]);
+        l[h] += p0;
+        l[h] += p1;
+        if constexpr (FOLD)
+          split2<BF>(p0, p1, pf[0][2 * n], pf[0][2 * n + 1]);
         else
-          pf[0][2 * n + h] = pack2<BF>(s[n][2 * h], s[n][2 * h + 1]);
+          split2<BF>(p0, p1, pf[0][2 * n + h], pf[1][2 * n + h]);
       }
-    }
 #pragma unroll
     for (int n = 0; n < DH / 16; ++n) {
       uint32_t b[4];
       ldmatrix4<true>(b, sv + vrow * kRowBytes + (((2 * n + vcol) ^ (vrow & 7)) << 4));
 #pragma unroll
-      for (int e = 0; e < TERMS; ++e) {
+      for (int e = 0; e < kTerms; ++e) {
         mma16816<BF>(o[2 * n], pf[e], b[0], b[1]);
         mma16816<BF>(o[2 * n + 1], pf[e], b[2], b[3]);
       }
@@ -307,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
   }
   cp_wait<0>();
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kHalves; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
   }
@@ -321,12 +331,17 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
 #pragma unroll
     for (int n = 0; n < DH / 8; ++n) {
       float* d = so + (warp * kRows + r) * DH + 8 * n + c;
-      *reinterpret_cast<float2*>(d) = make_float2(o[n][0], o[n][1]);
-      *reinterpret_cast<float2*>(d + 8 * DH) = make_float2(o[n][2], o[n][3]);
+      if constexpr (FOLD) {
+        *reinterpret_cast<float2*>(d) = make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+      } else {
+        *reinterpret_cast<float2*>(d) = make_float2(o[n][0], o[n][1]);
+        *reinterpret_cast<float2*>(d + 8 * DH) = make_float2(o[n][2], o[n][3]);
+      }
     }
     if ((lane & 3) == 0) {
-      sml[warp * kRows + r] = make_float2(m[0], l[0]);
-      sml[warp * kRows + r + 8] = make_float2(m[1], l[1]);
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        sml[warp * kRows + r + 8 * h] = make_float2(m[h], l[h]);
     }
   }
   __syncthreads();
@@ -476,8 +491,7 @@ tp_status decode(const WindowDecode& w, void* scratch, cudaStream_t stream) {
   a.pml = static_cast<float2*>(scratch);
   a.po = reinterpret_cast<float*>(static_cast<uint8_t*>(scratch) + (a.splits > 1 ? ml : 0));
   constexpr int smem = DecSmem<DH>::kBytes;
-  const bool two = w.b * w.heads * DH <= kTwoTermOutputs;
-  auto kern = two ? window_decode<BF, DH, 2> : window_decode<BF, DH, 1>;
+  auto kern = a.rows <= kFoldRows ? window_decode<BF, DH, true> : window_decode<BF, DH, false>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "window decode smem");
