@@ -435,10 +435,14 @@ tp_status tp_glu_fwd(const void* X, const void* Wgu, const void* bgu, const void
  *   dWd = H^T dZ;  dWgu = X^T [dG | dU];  dX = [dG | dU] Wgu^T (the shards'
  *   and both halves' partials summed in the accumulator);
  *   dbgu = colsum([dG | dU]);  dbd = colsum(dZ).
- *   GUsave (fp16): from the forward, or NULL to recompute it from X, Wgu, bgu.
+ *   GUsave (fp16): from the forward, or NULL to recompute it from X, Wgu, bgu;
+ *   the recomputed [G | U] is held in two bf16 terms (16 mantissa bits, the range
+ *   of bf16), so this is the way for pre-activations outside the fp16 range.
  *   [dG | dU] and H are rounded to bf16 for the products.  Outputs dX [M, h],
  *   dWgu [h, 2f], dWd [f, h], and dbgu [2f], dbd [h] when
  *   not NULL; all bf16.  Deterministic.
+ *   ws: tp_workspace_size(TP_OP_GLU_BWD, M, h, f, 0, t, TP_BF16) covers the
+ *   recomputation; with GUsave a workspace without its 8 M f bytes will do.
  * Errors: as tp_glu_fwd; NULL dZ / dX / dWgu / dWd.
  */
 tp_status tp_glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* Wd,

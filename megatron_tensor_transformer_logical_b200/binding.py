@@ -490,7 +490,8 @@ def tp_glu_fwd(X, Wgu, bgu, Wd, bd, Z, GUsave, t: int, act: int, ws, stream=None
 
 def tp_glu_bwd(X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t: int, act: int, ws,
                stream=None) -> None:
-    """Backward of tp_glu_fwd; GUsave None recomputes [G | U]; dbgu, dbd may be None."""
+    """Backward of tp_glu_fwd; GUsave None recomputes [G | U], in the range of bf16;
+    dbgu, dbd may be None."""
     dev, dt, M, h, f, x, wgu, wd = _glu_sizes(X, Wgu, Wd)
     if _current_device() != dev:
         return _elsewhere(dev, tp_glu_bwd, X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, t,

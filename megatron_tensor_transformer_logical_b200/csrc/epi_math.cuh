@@ -188,6 +188,18 @@ __device__ __forceinline__ uint4 pack8_f16(float* f, bool& clamped) {
   return u;
 }
 
+// Eight fp32 values as two bf16 terms: the rounded values and the rounded rests
+// (16 mantissa bits together, the range of fp32).
+__device__ __forceinline__ uint4 split8(const float* f, uint4& rest) {
+  const uint4 hi = pack8(f);
+  float h[8], r[8];
+  unpack8(hi, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = isinf(h[i]) ? 0.0f : f[i] - h[i];
+  rest = pack8(r);
+  return hi;
+}
+
 // Eight fp16 values as fp32.
 __device__ __forceinline__ void unpack8_f16(const uint4& u, float* f) {
   const __half2* p = reinterpret_cast<const __half2*>(&u);

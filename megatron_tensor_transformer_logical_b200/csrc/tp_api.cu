@@ -905,9 +905,10 @@ size_t glu_bwd_colsum_bytes(int64_t M, int64_t h, int64_t f) {
   return align_up(dba_partial_bytes(M, 2 * f), 256) + mlp_bias_grads_scratch_bytes(M, h);
 }
 
-size_t glu_bwd_ws_min(int64_t M, int64_t h, int64_t f) {
-  // [dG | dU], H, the recomputed [G | U], column sums
-  return 5 * align_up(M * f * 2, 256) + align_up(glu_bwd_colsum_bytes(M, h, f), 256) + 2048;
+// [dG | dU], H, column sums, and unless [G | U] was kept, its two bf16 terms.
+size_t glu_bwd_ws_min(int64_t M, int64_t h, int64_t f, bool kept) {
+  return (kept ? 3 : 7) * align_up(M * f * 2, 256) +
+         align_up(glu_bwd_colsum_bytes(M, h, f), 256) + 2048;
 }
 
 tp_status glu_check(int64_t M, int64_t h, int64_t f, int t, tp_act act, tp_dtype dtype) {
@@ -922,9 +923,11 @@ tp_status glu_check(int64_t M, int64_t h, int64_t f, int t, tp_act act, tp_dtype
   return check_rows({h, f});
 }
 
-// H = act(X Wg + bg) * (X Wu + bu), [G | U] (fp16) to GU unless nullptr.
-tp_status glu_up(const void* X, const void* Wgu, const void* bgu, void* H, void* GU, int64_t M,
-                 int64_t h, int64_t f, int t, tp_act act, const Tail& tail, cudaStream_t stream) {
+// H = act(X Wg + bg) * (X Wu + bu), [G | U] to GU unless nullptr: fp16, or with
+// GUrest two bf16 terms.
+tp_status glu_up(const void* X, const void* Wgu, const void* bgu, void* H, void* GU, void* GUrest,
+                 int64_t M, int64_t h, int64_t f, int t, tp_act act, const Tail& tail,
+                 cudaStream_t stream) {
   Gemm g;
   g.M = M; g.N = f; g.K = h;
   g.a = {X, h, true};
@@ -934,6 +937,7 @@ tp_status glu_up(const void* X, const void* Wgu, const void* bgu, void* H, void*
   g.out = H; g.ldo = f;
   g.bias = bgu;
   g.out2 = GU; g.ldo2 = 2 * f;
+  g.rest = GUrest;
   g.n_shard = f / t;
   tail.to(g);
   return launch_gemm_bf16(g, stream);
@@ -958,7 +962,7 @@ tp_status glu_fwd(const void* X, const void* Wgu, const void* bgu, const void* W
     return launch_thin_glu(g, stream);
   }
   const Tail tail(c);
-  TP_TRY(glu_up(X, Wgu, bgu, H, GUsave, M, h, f, t, act, tail, stream));
+  TP_TRY(glu_up(X, Wgu, bgu, H, GUsave, nullptr, M, h, f, t, act, tail, stream));
   // Row-split second linear: the shards' products are summed in the accumulator.
   Gemm g2;
   g2.M = M; g2.N = h; g2.K = f;
@@ -978,18 +982,19 @@ tp_status glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* W
     return fail(TP_ERR_NULL, "X, Wgu, Wd, dZ, dX, dWgu and dWd are required");
   TP_TRY(glu_check(M, h, f, t, act, dtype));
   TP_TRY(check_ptrs_aligned({X, Wgu, bgu, Wd, GUsave, dZ, dX, dWgu, dbgu, dWd, dbd, ws}));
-  if (ws == nullptr || ws_bytes < glu_bwd_ws_min(M, h, f))
+  if (ws == nullptr || ws_bytes < glu_bwd_ws_min(M, h, f, GUsave != nullptr))
     return fail(TP_ERR_WORKSPACE, "workspace missing or smaller than tp_workspace_size()");
   Carve c(ws, ws_bytes);
   void* dGU = c.take(M * 2 * f * 2);
   void* H = c.take(M * f * 2);
-  void* GUrec = c.take(M * 2 * f * 2);
+  void* GUrec = GUsave != nullptr ? nullptr : c.take(M * 2 * f * 2);
+  void* GUrest = GUsave != nullptr ? nullptr : c.take(M * 2 * f * 2);
   void* scratch = c.take(glu_bwd_colsum_bytes(M, h, f));
   const Tail tail(c);
 
   const void* GU = GUsave;
   if (GU == nullptr) {
-    TP_TRY(glu_up(X, Wgu, bgu, H, GUrec, M, h, f, t, act, tail, stream));
+    TP_TRY(glu_up(X, Wgu, bgu, H, GUrec, GUrest, M, h, f, t, act, tail, stream));
     GU = GUrec;
   }
   // dH_i = dZ Wd_i^T per column shard; the epilogue turns it into [dG | dU]
@@ -1001,6 +1006,7 @@ tp_status glu_bwd(const void* X, const void* Wgu, const void* bgu, const void* W
   g1.epi = kEpiDGlu;
   g1.act = act;
   g1.aux = GU; g1.ldaux = 2 * f;
+  g1.rest = GUrest;
   g1.out = dGU; g1.ldo = 2 * f;
   g1.out2 = GUsave != nullptr ? H : nullptr; g1.ldo2 = f;
   g1.n_shard = f / t;
@@ -1461,7 +1467,7 @@ size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, i
       case TP_OP_GLU_FWD:
       case TP_OP_GLU_BWD:
         if (f <= 0 || f > kMaxDim / 2 || dtype != TP_BF16) return 0;
-        return (op == TP_OP_GLU_FWD ? glu_fwd_ws_min(M, f) : glu_bwd_ws_min(M, h, f)) + tail_ws();
+        return (op == TP_OP_GLU_FWD ? glu_fwd_ws_min(M, f) : glu_bwd_ws_min(M, h, f, false)) + tail_ws();
       case TP_OP_QK_NORM_ROPE_BWD: break;  // answered above
     }
   } catch (...) {

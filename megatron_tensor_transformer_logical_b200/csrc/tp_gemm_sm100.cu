@@ -131,6 +131,7 @@ struct Args {
   // boxes and the tensor maps tmO (out), tmO2 (out2) and tmX (aux).
   int tma_out;
   int act;  // kEpiGlu / kEpiDGlu: the activation (tp_act)
+  __nv_bfloat16* rest;  // kEpiGlu / kEpiDGlu: second bf16 term of [g | u], or nullptr (fp16)
   // kEpiDGelu / kEpiDGlu only: column sums of the output (fp32, before rounding) per
   // 32-row group, csum_part[(row / 32) * csum_ld + col]; nullptr: none.
   float* csum_part;
@@ -335,11 +336,48 @@ __device__ __forceinline__ void glu_colsum(float (&v)[32], int row, int ncols, i
     a.csum_part[static_cast<long long>(row >> 5) * a.csum_ld + pcol0 + lane] = sum;
 }
 
+// Eight values of g and of u at `off` of [g | u] (u half a row on): fp16, or two
+// bf16 terms.
+__device__ __forceinline__ void store_gu8(float* g, float* u, long long off, const Args& a,
+                                          bool& clamped) {
+  uint4 x, y;
+  if (a.rest != nullptr) {
+    uint4 xr, yr;
+    x = split8(g, xr);
+    y = split8(u, yr);
+    *reinterpret_cast<uint4*>(a.rest + off) = xr;
+    *reinterpret_cast<uint4*>(a.rest + off + a.N) = yr;
+  } else {
+    x = pack8_f16(g, clamped);
+    y = pack8_f16(u, clamped);
+  }
+  *reinterpret_cast<uint4*>(a.out2 + off) = x;
+  *reinterpret_cast<uint4*>(a.out2 + off + a.N) = y;
+}
+
+// Eight values of g and of u from what is kept of them, the rests at `off`.
+__device__ __forceinline__ void unpack_gu8(const uint4& x, const uint4& y, long long off,
+                                           const Args& a, float* g, float* u) {
+  if (a.rest != nullptr) {
+    float r[8];
+    unpack8(x, g);
+    unpack8(*reinterpret_cast<const uint4*>(a.rest + off), r);
+    add8(g, r);
+    unpack8(y, u);
+    unpack8(*reinterpret_cast<const uint4*>(a.rest + off + a.N), r);
+    add8(u, r);
+  } else {
+    unpack8_f16(x, g);
+    unpack8_f16(y, u);
+  }
+}
+
 // kEpiGlu on 32 columns of one row with direct stores: g, u the two products.
-// [g | u] is kept in fp16: three more mantissa bits than bf16 halve the
-// backward's rounding error (gradients 3.5e-3 -> 2.4e-3 from exact, where
-// their own rounding is 1.7e-3); values past the fp16 range are saturated and
-// flagged, as the attention's fp16 intermediates are.
+// What a caller keeps of [g | u] is fp16: three more mantissa bits than bf16
+// halve the backward's rounding error (gradients 3.5e-3 -> 2.4e-3 from exact,
+// where their own rounding is 1.7e-3); values past the fp16 range are saturated
+// and flagged, as the attention's fp16 intermediates are.  A backward that
+// recomputes it takes two bf16 terms, which have bf16's range.
 __device__ __forceinline__ void epilogue_glu_row32(float (&g)[32], float (&u)[32], int row,
                                                    int col0, int col_end, const Args& a) {
   if (row >= a.M) return;
@@ -362,11 +400,7 @@ __device__ __forceinline__ void epilogue_glu_row32(float (&g)[32], float (&u)[32
     mul8(h, y);
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + col) =
         pack8(h);
-    if (a.out2 != nullptr) {  // two-byte elements, fp16 here
-      __nv_bfloat16* o2 = a.out2 + (long long)row * a.ldo2 + col;
-      *reinterpret_cast<uint4*>(o2) = pack8_f16(x, clamped);
-      *reinterpret_cast<uint4*>(o2 + a.N) = pack8_f16(y, clamped);
-    }
+    if (a.out2 != nullptr) store_gu8(x, y, (long long)row * a.ldo2 + col, a, clamped);
   }
   if (clamped) status_flag(a.status, kFlagF16Range);
 }
@@ -384,10 +418,10 @@ __device__ __forceinline__ void epilogue_dglu_row32(float (&v)[32], float (&du)[
       for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.0f;
       continue;
     }
-    const __nv_bfloat16* gp = a.aux + (long long)row * a.ldaux + col;
+    const long long off = (long long)row * a.ldaux + col;
     float g[8], u[8], h[8];
-    unpack8_f16(*reinterpret_cast<const uint4*>(gp), g);  // two-byte elements, fp16 here
-    unpack8_f16(*reinterpret_cast<const uint4*>(gp + a.N), u);
+    unpack_gu8(*reinterpret_cast<const uint4*>(a.aux + off),
+               *reinterpret_cast<const uint4*>(a.aux + off + a.N), off, a, g, u);
     dglu8(x, g, u, a.act, y, h);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + col;
     *reinterpret_cast<uint4*>(o) = pack8(x);
@@ -647,7 +681,16 @@ __device__ __forceinline__ void epilogue_glu_boxed(uint32_t tg, uint32_t tu, int
                          __shfl_sync(0xffffffffu, bu.w, bl0 + q)), bb);
       add8(y, bb);
     }
-    if (a.out2 != nullptr) {
+    if (a.out2 != nullptr && a.rest != nullptr) {
+      uint4 xr, yr;  // the rests leave directly
+      *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)) = split8(x, xr);
+      *reinterpret_cast<uint4*>(box1 + sw64_off(lane, q)) = split8(y, yr);
+      if (row0 + lane < a.M) {
+        __nv_bfloat16* r = a.rest + (long long)(row0 + lane) * a.ldo2 + col + 8 * q;
+        *reinterpret_cast<uint4*>(r) = xr;
+        *reinterpret_cast<uint4*>(r + a.N) = yr;
+      }
+    } else if (a.out2 != nullptr) {
       float gs[8], us[8];  // what is kept may be saturated, h is not
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -701,8 +744,8 @@ __device__ __forceinline__ bool epilogue_dglu_boxed(uint32_t taddr, int lane, in
     uint4* p0 = reinterpret_cast<uint4*>(box0 + sw64_off(lane, q));
     uint4* p1 = reinterpret_cast<uint4*>(box1 + sw64_off(lane, q));
     float g[8], u[8], h[8];
-    unpack8_f16(*p0, g);
-    unpack8_f16(*p1, u);
+    // rows past M read the last row's rests; the boxes clip them when they leave
+    unpack_gu8(*p0, *p1, (long long)min(row, a.M - 1) * a.ldaux + col + 8 * q, a, g, u);
     dglu8(v + 8 * q, g, u, a.act, du + 8 * q, h);
     *p0 = pack8(v + 8 * q);
     *p1 = pack8(du + 8 * q);
@@ -1646,6 +1689,7 @@ tp_status launch_impl(const Gemm& g, cudaStream_t stream) {
   a.csum_part = (EPI == kEpiDGelu || EPI == kEpiDGlu) ? g.csum_part : nullptr;
   a.csum_ld = EPI == kEpiDGlu ? 2 * g.N : g.N;
   a.act = g.act;
+  a.rest = static_cast<__nv_bfloat16*>(g.rest);
   a.status = wait_ctl();
   if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
   EpiMaps em;
@@ -1748,6 +1792,7 @@ tp_status launch_pair(const Gemm& g, cudaStream_t stream) {
   a.csum_part = (EPI == kEpiDGelu || EPI == kEpiDGlu) ? g.csum_part : nullptr;
   a.csum_ld = EPI == kEpiDGlu ? 2 * g.N : g.N;
   a.act = g.act;
+  a.rest = static_cast<__nv_bfloat16*>(g.rest);
   a.status = wait_ctl();
   if (a.status.st == nullptr) return fail(TP_ERR_CUDA, "device status unavailable");
   EpiMaps em;

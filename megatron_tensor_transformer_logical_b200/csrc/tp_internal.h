@@ -129,6 +129,10 @@ struct Gemm {
   // that hold both halves ([Wg | Wu], [g | u] and its gradient) have 2 N
   // columns, the second half at column N.  act: tp_act.
   int act = TP_ACT_SILU;
+  // kEpiGlu / kEpiDGlu: nullptr, and [g | u] in out2 / aux is fp16 (saturated,
+  // flagged); or the second of two bf16 matrices, out2 / aux and the rests, whose
+  // sum it is (same leading dimension).
+  void* rest = nullptr;
   KOrder korder;
   CEOut ce;                    // kEpiCE only (requires n_shard % 8 == 0)
   // kEpiDGelu / kEpiDGlu on the tensor-core path: per-32-row column sums of the output
