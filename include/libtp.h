@@ -47,7 +47,7 @@
  * - No C++ exception crosses this interface.  A non-TP_OK status leaves a
  *   message for tp_last_error().  TP_ERR_CUDA reports a launch error.  Errors
  *   that kernels detect while running (a bounded wait that expired) and
- *   conditions they flag (an fp16 intermediate saturated) are recorded in a
+ *   conditions they flag (an fp16 intermediate out of its range) are recorded in a
  *   per-device status, read by tp_device_status().  Neither stops a later
  *   call: a flag is never read by a kernel, and a timeout makes only the
  *   other waits of its own launch give up early (each launch carries its own
@@ -412,9 +412,12 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  * products with Wd are summed in its accumulator.
  *   X [M, h]; bgu [2f] = [bg | bu] or NULL; Wd [f, h]; bd [h] or NULL;
  *   Z [M, h]; GUsave [M, 2f] fp16 = [G | U] or NULL: kept for the backward
- *   (fp16 keeps three more mantissa bits than bf16; a value beyond its range
- *   is saturated there and reported by tp_device_status() as TP_ERR_KERNEL,
- *   Z is not affected).  H lives in the workspace, rounded to bf16 (up to 8
+ *   (fp16 keeps three more mantissa bits than bf16; a value beyond its range,
+ *   an infinity too, is saturated there, and where the largest of 32
+ *   neighbouring values of a token's G or U is not 0 but below 2^-17, fp16 is
+ *   coarser than bf16; both are reported by tp_device_status() as
+ *   TP_ERR_KERNEL.  Z is not affected, and a backward without GUsave covers
+ *   bf16's range).  H lives in the workspace, rounded to bf16 (up to 8
  *   tokens with the rounded rest as a second term).
  *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
@@ -645,8 +648,9 @@ const char* tp_last_error(void);
 /*
  * Synchronizes `stream`, then reads and clears the status of the current
  * device.  TP_OK, TP_ERR_KERNEL (a kernel gave up a bounded wait since the
- * last read, or an fp16 attention intermediate was saturated; the message
- * says which, a timeout first) or TP_ERR_CUDA.  Outputs of the launch that
+ * last read, an fp16 intermediate was saturated, or the gated block's kept
+ * pre-activations were too low for fp16; the message says which, a timeout
+ * first) or TP_ERR_CUDA.  Outputs of the launch that
  * gave up a wait are incomplete; outputs of every other launch are not
  * affected.  The same launch replayed from a captured CUDA graph keeps its
  * generation, so after a timeout read this before replaying the graph.

@@ -168,6 +168,19 @@ __device__ __forceinline__ uint4 pack8(const float* f) {
 
 constexpr float kF16Max = 65504.0f;
 
+// fp16 is spaced 2^-24 apart below 2^-14, so where the largest of 32 neighbouring
+// values is below 2^-17, what is kept of it is coarser than bf16 (half a step,
+// 2^-25, is over 2^-8 of it).  Zeros are kept exactly.
+constexpr float kF16Small = 7.62939453125e-6f;
+__device__ __forceinline__ bool f16_too_small(float largest) {
+  return largest > 0.0f && largest < kF16Small;
+}
+__device__ __forceinline__ float absmax8(const float* f, float m) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+  return m;
+}
+
 // Eight fp32 values to fp16, saturated to the finite range; returns whether
 // any finite value had to be clamped.
 __device__ __forceinline__ uint4 pack8_f16(float* f, bool& clamped) {

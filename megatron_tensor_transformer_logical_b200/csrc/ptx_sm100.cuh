@@ -21,6 +21,7 @@ enum : int {
 // Bits of DeviceStatus::flags: conditions that are reported but stop nothing.
 enum : int {
   kFlagF16Range = 0x1,  // a value outside the fp16 range was saturated
+  kFlagF16Small = 0x2,  // neighbouring values all lay too low in the fp16 range
 };
 
 // Per-device status, one instance in device memory.  Timeouts and flags are

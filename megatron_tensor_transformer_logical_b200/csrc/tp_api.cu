@@ -1495,7 +1495,11 @@ tp_status tp_device_status(void* stream) {
                                                   "dO, the gated block's saved [G | U]) exceeded "
                                                   "the fp16 range and was saturated"
                                                 : "";
-    char buf[256];
+    const char* low = (v.flags & kFlagF16Small) ? "; 32 neighbouring values of the gated block's "
+                                                  "saved [G | U] lay below 2^-17, where fp16 is "
+                                                  "coarser than bf16"
+                                                : "";
+    char buf[512];
     if (v.code != 0) {
       const char* who = v.code == kStatusProducerTimeout   ? "GEMM TMA producer"
                         : v.code == kStatusMmaTimeout      ? "GEMM MMA issuer"
@@ -1503,14 +1507,12 @@ tp_status tp_device_status(void* stream) {
                         : v.code == kStatusAttnTimeout     ? "attention kernel"
                         : v.code == kStatusSelftestTimeout ? "bounded-wait self-test"
                                                            : "unknown";
-      std::snprintf(buf, sizeof(buf), "kernel gave up a bounded wait (code 0x%x, %s)%s", v.code,
-                    who, sat);
+      std::snprintf(buf, sizeof(buf), "kernel gave up a bounded wait (code 0x%x, %s)%s%s", v.code,
+                    who, sat, low);
       return fail(TP_ERR_KERNEL, buf);
     }
-    if (v.flags & kFlagF16Range) {
-      std::snprintf(buf, sizeof(buf),
-                    "an fp16 attention intermediate (QKV or dO) exceeded the fp16 range and was "
-                    "saturated (flags 0x%x)", v.flags);
+    if (v.flags & (kFlagF16Range | kFlagF16Small)) {
+      std::snprintf(buf, sizeof(buf), "flags 0x%x%s%s", v.flags, sat, low);
       return fail(TP_ERR_KERNEL, buf);
     }
     return TP_OK;

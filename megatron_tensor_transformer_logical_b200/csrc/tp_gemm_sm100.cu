@@ -336,10 +336,30 @@ __device__ __forceinline__ void glu_colsum(float (&v)[32], int row, int ncols, i
     a.csum_part[static_cast<long long>(row >> 5) * a.csum_ld + pcol0 + lane] = sum;
 }
 
+// What the fp16 form of [g | u] does to the values of a thread: whether any was
+// saturated, and the largest |g| and |u|.
+struct F16Seen {
+  bool clamped = false;
+  float g = 0.0f, u = 0.0f;
+  __device__ __forceinline__ void flag(const Args& a) const {
+    const int bits = (clamped ? kFlagF16Range : 0) |
+                     (f16_too_small(g) || f16_too_small(u) ? kFlagF16Small : 0);
+    if (bits) status_flag(a.status, bits);
+  }
+};
+
+// Eight values of g and of u as fp16, saturated (g and u themselves too).
+__device__ __forceinline__ void pack_gu8(float* g, float* u, uint4& x, uint4& y, F16Seen& seen) {
+  seen.g = absmax8(g, seen.g);
+  seen.u = absmax8(u, seen.u);
+  x = pack8_f16(g, seen.clamped);
+  y = pack8_f16(u, seen.clamped);
+}
+
 // Eight values of g and of u at `off` of [g | u] (u half a row on): fp16, or two
 // bf16 terms.
 __device__ __forceinline__ void store_gu8(float* g, float* u, long long off, const Args& a,
-                                          bool& clamped) {
+                                          F16Seen& seen) {
   uint4 x, y;
   if (a.rest != nullptr) {
     uint4 xr, yr;
@@ -348,8 +368,7 @@ __device__ __forceinline__ void store_gu8(float* g, float* u, long long off, con
     *reinterpret_cast<uint4*>(a.rest + off) = xr;
     *reinterpret_cast<uint4*>(a.rest + off + a.N) = yr;
   } else {
-    x = pack8_f16(g, clamped);
-    y = pack8_f16(u, clamped);
+    pack_gu8(g, u, x, y, seen);
   }
   *reinterpret_cast<uint4*>(a.out2 + off) = x;
   *reinterpret_cast<uint4*>(a.out2 + off + a.N) = y;
@@ -376,12 +395,13 @@ __device__ __forceinline__ void unpack_gu8(const uint4& x, const uint4& y, long 
 // What a caller keeps of [g | u] is fp16: three more mantissa bits than bf16
 // halve the backward's rounding error (gradients 3.5e-3 -> 2.4e-3 from exact,
 // where their own rounding is 1.7e-3); values past the fp16 range are saturated
-// and flagged, as the attention's fp16 intermediates are.  A backward that
-// recomputes it takes two bf16 terms, which have bf16's range.
+// and flagged, as the attention's fp16 intermediates are, and so are 32
+// neighbours too low in it.  A backward that recomputes [g | u] takes two bf16
+// terms, which have bf16's range.
 __device__ __forceinline__ void epilogue_glu_row32(float (&g)[32], float (&u)[32], int row,
                                                    int col0, int col_end, const Args& a) {
   if (row >= a.M) return;
-  bool clamped = false;
+  F16Seen seen;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int col = col0 + 8 * q;
@@ -400,9 +420,9 @@ __device__ __forceinline__ void epilogue_glu_row32(float (&g)[32], float (&u)[32
     mul8(h, y);
     *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + (long long)row * a.ldo + col) =
         pack8(h);
-    if (a.out2 != nullptr) store_gu8(x, y, (long long)row * a.ldo2 + col, a, clamped);
+    if (a.out2 != nullptr) store_gu8(x, y, (long long)row * a.ldo2 + col, a, seen);
   }
-  if (clamped) status_flag(a.status, kFlagF16Range);
+  seen.flag(a);
 }
 
 // kEpiDGlu on 32 columns of one row with direct loads and stores; leaves dg
@@ -664,7 +684,7 @@ __device__ __forceinline__ void epilogue_glu_boxed(uint32_t tg, uint32_t tu, int
   float g[32], u[32];
   tmem_ld32(tg, g);
   tmem_ld32(tu, u);
-  bool clamped = false;
+  F16Seen seen;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float *x = g + 8 * q, *y = u + 8 * q;
@@ -697,11 +717,11 @@ __device__ __forceinline__ void epilogue_glu_boxed(uint32_t tg, uint32_t tu, int
         gs[i] = x[i];
         us[i] = y[i];
       }
-      *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)) = pack8_f16(gs, clamped);
-      *reinterpret_cast<uint4*>(box1 + sw64_off(lane, q)) = pack8_f16(us, clamped);
+      pack_gu8(gs, us, *reinterpret_cast<uint4*>(box0 + sw64_off(lane, q)),
+               *reinterpret_cast<uint4*>(box1 + sw64_off(lane, q)), seen);
     }
   }
-  if (clamped) status_flag(a.status, kFlagF16Range);
+  if (row0 + lane < a.M) seen.flag(a);
   if (a.out2 != nullptr)
     box_flush(lane, true, [&] {
       tma_store_2d(tmO2, box0, col, row0);

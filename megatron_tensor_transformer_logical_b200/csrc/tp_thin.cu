@@ -293,7 +293,23 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
         bool clamped = false;
         *reinterpret_cast<__half2*>(p) = sat_half2(g, clamped);
         *reinterpret_cast<__half2*>(p + a.N) = sat_half2(u, clamped);
-        if (clamped) status_flag(a.status, kFlagF16Range);
+        // A warp holds the 64 columns of one token, lanes past N left out; the
+        // largest values of each 32, in 16 lanes.
+        static_assert(kCols == 64, "a warp's columns");
+        const int here = min(32, (a.N - tcol) / 2);
+        const unsigned mask = 0xffffffffu >> (32 - here);
+        float mg = fmaxf(fabsf(g.x), fabsf(g.y)), mu = fmaxf(fabsf(u.x), fabsf(u.y));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+          const float vg = __shfl_xor_sync(mask, mg, o), vu = __shfl_xor_sync(mask, mu, o);
+          if ((lane ^ o) < here) {
+            mg = fmaxf(mg, vg);
+            mu = fmaxf(mu, vu);
+          }
+        }
+        const int bits = (clamped ? kFlagF16Range : 0) |
+                         (f16_too_small(mg) || f16_too_small(mu) ? kFlagF16Small : 0);
+        if (bits) status_flag(a.status, bits);
       }
       const float2 h = __fmul2_rn(gate_act2(g, a.act), u);
       const __nv_bfloat162 hi = __floats2bfloat162_rn(h.x, h.y);

@@ -113,3 +113,37 @@ def test_kept_preactivations_need_no_room_for_recomputed_ones():
     with pytest.raises(L.TPError) as e:
         L.tp_glu_bwd(*args, None, *grads, buf[:need])
     assert e.value.status == L.TP_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("M", [1, 5, 20, 90, 260])
+@pytest.mark.parametrize("h,f", [(64, 72), (128, 264)])
+def test_kept_preactivations_too_low_for_fp16_are_flagged(M, h, f):
+    """[G | U] is kept in fp16, whose steps stay 2^-24 below 2^-14: 32 neighbours
+    that all lie below 2^-17 are reported, those of one token and of U alone too;
+    zeros, which are exact, and values of order one are not."""
+    d = make(M, h, f, False, seed=25)
+
+    def status():
+        run(d, 1, "silu", backward=False)
+        try:
+            L.tp_device_status()
+        except L.TPError as e:
+            assert e.status == L.TP_ERR_KERNEL and "2^-17" in str(e)
+            return True
+        return False
+
+    assert not status()
+    last = d["X"][M - 1].clone()
+    d["X"][M - 1] = 0
+    assert not status()
+    d["X"][M - 1] = last * 2.0 ** -22  # G and U of that token about 2^-22
+    assert status()
+    run(d, 1, "silu", save=False, backward=False)
+    L.tp_device_status()  # nothing kept, nothing to report
+    d["X"][M - 1] = last
+    d["Wgu"][:, f:] *= 2.0 ** -22  # U alone
+    assert status()
+    d["Wgu"][:, f:] = 0
+    assert not status()
+    d["Wgu"][:, f + 32:f + 64] = 2.0 ** -30  # one run of 32 columns
+    assert status()
