@@ -417,11 +417,14 @@ tp_status tp_vocab_ce_bwd(const void* X, const void* E, const int32_t* targets,
  *   neighbouring values of a token's G or U is not 0 but below 2^-17, fp16 is
  *   coarser than bf16; both are reported by tp_device_status() as
  *   TP_ERR_KERNEL.  Z is not affected, and a backward without GUsave covers
- *   bf16's range).  H lives in the workspace, rounded to bf16 (up to 8
- *   tokens with the rounded rest as a second term).
+ *   bf16's range).  H lives in the workspace, rounded to bf16; up to 8
+ *   tokens, where it costs little, the rounded rest is a second term, and Z is
+ *   off by its own rounding instead of 1.4 times that.
  *   Up to 32 tokens take kernels that stream the weights once (a token's
  *   cost is reading them); their sums are grouped differently from the
- *   larger batches'.
+ *   larger batches'.  So a token's Z differs, within these roundings, between
+ *   batches of up to 8, up to 32 and more tokens; among batches of up to 8, or
+ *   of 9 to 32, it is the same whatever their size.
  *   ws: tp_workspace_size(TP_OP_GLU_FWD, M, h, f, 0, t, TP_BF16); what serves M
  *   tokens also serves fewer.
  * Errors: NULL X / Wgu / Wd / Z; f % t; alignment (h, f multiples of 8);

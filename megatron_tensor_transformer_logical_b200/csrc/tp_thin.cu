@@ -14,11 +14,13 @@
 //   (a cluster of blocks) through distributed shared memory, in a fixed
 //   order; then bias, activation and product.  Nothing goes through HBM but
 //   the weights, X, H and Z.
-// * Up to 8 tokens H goes from one product to the other as two bf16 terms, the
-//   rounded value and the rounded rest (60.4 against 59.2 us for one token):
-//   few outputs do not average, and Z is then off by its own rounding alone,
-//   not by 1.4 times that.  At 13 tokens the second term would cost 6% (25.1
-//   against 23.6 us), at 32 tokens 12%.
+// * H is rounded to bf16 between the products, as in the larger batches' GEMM,
+//   which makes a token's Z 1.4 times as far off as its own rounding.  Up to 8
+//   tokens the rounded rest follows as a second term, because it is nearly free
+//   there: 60.4 against 59.2 us for one token, 66 for 8 (9 with one term 64).
+//   That is a trade of speed alone, a token's accuracy does not gain from
+//   company: at 13 tokens the second term would cost 6% (25.1 against 23.6 us),
+//   at 32 tokens 12%, in the GEMM another product.
 // * The down product is launched with programmatic stream serialisation: its
 //   blocks start as the up product's finish, request their first weight tiles,
 //   and only then wait for H.

@@ -147,3 +147,24 @@ def test_kept_preactivations_too_low_for_fp16_are_flagged(M, h, f):
     assert not status()
     d["Wgu"][:, f + 32:f + 64] = 2.0 ** -30  # one run of 32 columns
     assert status()
+
+
+def test_both_sides_of_the_few_token_choices():
+    """The same tokens in batches of 1, 8, 9, 16, 17, 32, 33 and 70: up to 8 H has
+    two terms (2^-16 of it stays) and Z is off by its own rounding, beyond by H's
+    too; among batches of up to 8, and of 9 to 32, a token's Z is the same."""
+    h, f = 520, 1416
+    d = make(70, h, f, True, seed=26)
+    ref, tol = kept_reference(d, "silu")
+    G, U = ref["GU"].split(f, 1)
+    cut = (HS - 2.0 ** -16) * ((act(G, "silu")[0] * U).abs() @ d["Wd"].double().abs())
+    Z = {}
+    for M in (1, 8, 9, 16, 17, 32, 33, 70):
+        part = dict(d, X=d["X"][:M].contiguous(), dZ=d["dZ"][:M].contiguous())
+        Z[M] = run(part, 1, "silu", save=False, backward=False)["Z"]
+        t = tol["Z"][:M] - (cut[:M] if M <= 8 else 0)
+        over = ((Z[M].double() - ref["Z"][:M]).abs() - t).max().item()
+        assert over <= 0, f"{M} tokens: {over:.3e} over the bound"
+    assert torch.equal(Z[1], Z[8][:1])
+    for M in (9, 16, 17):
+        assert torch.equal(Z[M], Z[32][:M])
