@@ -24,7 +24,10 @@
 // * The down product is launched with programmatic stream serialisation: its
 //   blocks start as the up product's finish, request their first weight tiles,
 //   and only then wait for H.
-// All blocks run at once, two per SM (clusters are sized for that).
+// Clusters are sized so that all blocks run at once, two per SM.  From 2 SMs of
+// tiles on (f above 18944 on 148 SMs) a tile is one block and the rest of them
+// run as the first ones leave: 8192 x 28672, one token (1409 MB, 448 up tiles)
+// 223 us, 6.3 TB/s.
 // Measured: one token, h = 4096, f = 14336 (352 MB of weights) 60 us, 5.8 TB/s
 // over both products; 13 tokens, h = 2048, f = 5632 (69 MB) 23.6 us.  Tried on
 // these: five stages 61 / 23.7 us, three 62 / 24.1; clusters up to 16 blocks
@@ -32,7 +35,8 @@
 // per block with partial sums through HBM, joined by the last block of a tile,
 // 73 / 51.  Against the tcgen05 GEMM, whose 128-row tiles read the same
 // weights: 32 tokens 82 against 84 us (h = 2048: 31 against 39), 64 tokens 150
-// against 88 (52 against 40), so this path ends at 32.
+// against 88 (52 against 40), so this path ends at 32 (too late for the widest
+// blocks: 8192 x 28672, 32 tokens 288 us here, 33 by the GEMM 228).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -168,3 +168,13 @@ def test_both_sides_of_the_few_token_choices():
     assert torch.equal(Z[1], Z[8][:1])
     for M in (9, 16, 17):
         assert torch.equal(Z[M], Z[32][:M])
+
+
+@pytest.mark.parametrize("M", [3, 13, 32])
+def test_wide_blocks_take_more_than_one_round(M):
+    """448 tiles of the up product, and 313 of the down, where 296 blocks run at once."""
+    for h, f in ((128, 28672), (40000, 64)):
+        d = make(M, h, f, False, seed=27)
+        ref, tol = kept_reference(d, "silu")
+        out = run(d, 1, "silu", backward=False)
+        compare(out, ref, tol)
