@@ -611,7 +611,9 @@ typedef enum tp_kernel_kind {
   TP_KIND_ATTN_BWD = 3,      /* attention core backward (all its kernels)    */
   TP_KIND_REDUCE = 4,        /* column sums, row terms                       */
   TP_KIND_VOCAB = 5,         /* embedding gather / scatter, loss reductions  */
-  TP_KIND_COUNT = 6
+  TP_KIND_GEMM_STREAM = 6,   /* bf16 products of a few tokens (mma.sync), bound */
+                             /* by streaming the weights                     */
+  TP_KIND_COUNT = 7
 } tp_kernel_kind;
 
 typedef struct tp_profile_stats {
@@ -632,7 +634,8 @@ int64_t tp_launch_count(void);
 typedef struct tp_launch_record {
   int kind;            /* tp_kernel_kind                                        */
   int tile;            /* GEMM tile: 128/192/256 columns on one SM, 512 = 256x256 */
-                       /* on an SM pair.  TP_KIND_VOCAB: 1 embedding gather,    */
+                       /* on an SM pair.  TP_KIND_GEMM_STREAM: 16 or 32 tokens. */
+                       /* TP_KIND_VOCAB: 1 embedding gather,                    */
                        /* 2 embedding scatter-add, 3 loss combination, 4 the    */
                        /* softmax gradient.  0 for other kernels                */
   int64_t m, n, k;     /* GEMM problem size (0 for other kernels)               */

@@ -26,10 +26,10 @@ TP_OP_VOCAB_EMBED_BWD, TP_OP_QK_NORM_ROPE_BWD, TP_OP_GLU_FWD, TP_OP_GLU_BWD = 8,
 TP_ACT_SILU, TP_ACT_GELU = 0, 1
 
 (TP_KIND_GEMM_TCGEN05, TP_KIND_GEMM_SIMT, TP_KIND_ATTN_FWD, TP_KIND_ATTN_BWD, TP_KIND_REDUCE,
- TP_KIND_VOCAB) = range(6)
+ TP_KIND_VOCAB, TP_KIND_GEMM_STREAM) = range(7)
 KIND_NAMES = {TP_KIND_GEMM_TCGEN05: "gemm_tcgen05", TP_KIND_GEMM_SIMT: "gemm_simt",
               TP_KIND_ATTN_FWD: "attn_fwd", TP_KIND_ATTN_BWD: "attn_bwd", TP_KIND_REDUCE: "reduce",
-              TP_KIND_VOCAB: "vocab"}
+              TP_KIND_VOCAB: "vocab", TP_KIND_GEMM_STREAM: "gemm_stream"}
 
 EXPORTS = ("tp_linear_col", "tp_linear_row", "tp_mlp_fwd", "tp_mlp_bwd", "tp_attn_fwd",
            "tp_attn_bwd", "tp_workspace_size", "tp_last_error", "tp_device_status",

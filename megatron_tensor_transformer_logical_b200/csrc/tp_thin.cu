@@ -386,7 +386,7 @@ tp_status launch(ThinArgs a, bool pdl, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = na;
   const double cols = (GLU ? 2.0 : 1.0) * a.N;
-  LaunchScope scope(TP_KIND_GEMM_TCGEN05, 2.0 * a.M * a.K * cols,
+  LaunchScope scope(TP_KIND_GEMM_STREAM, 2.0 * a.M * a.K * cols,
                     2.0 * (a.K * cols + double(a.M) * a.K + double(a.M) * a.N), stream, 1, 16 * MT,
                     a.M, a.N, a.K);
   e = cudaLaunchKernelEx(&cfg, kern, a);

@@ -178,3 +178,19 @@ def test_wide_blocks_take_more_than_one_round(M):
         ref, tol = kept_reference(d, "silu")
         out = run(d, 1, "silu", backward=False)
         compare(out, ref, tol)
+
+
+def test_the_profile_tells_streamed_products_from_the_tensor_core_gemm():
+    h, f = 256, 512
+    for M, kind in ((4, L.TP_KIND_GEMM_STREAM), (20, L.TP_KIND_GEMM_STREAM),
+                    (40, L.TP_KIND_GEMM_TCGEN05)):
+        d = make(M, h, f, False, seed=28)
+        L.tp_profile_enable(True)
+        try:
+            run(d, 1, "silu", save=False, backward=False)
+            records = L.tp_profile_records()
+        finally:
+            L.tp_profile_enable(False)
+        assert [r["kind"] for r in records] == [L.KIND_NAMES[kind]] * 2
+        assert [r["flops"] for r in records] == [4.0 * M * h * f, 2.0 * M * h * f]
+        assert L.tp_profile_read(kind)["launches"] == 2
