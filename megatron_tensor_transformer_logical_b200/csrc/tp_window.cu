@@ -1566,11 +1566,11 @@ WinArgs base_args(const WindowAttn& w) {
 double visible_pairs(const WindowAttn& w) {
   double n = 0;
   const double off = double(w.sk - w.sq);
-  // rows with p + 1 <= window see p + 1 keys, later ones window + sinks
+  // rows with p + 1 <= window + sinks see p + 1 keys, later ones window + sinks
   const double p0 = std::max(0.0, off), p1 = double(w.sk);  // positions [p0, p1)
-  const double m = std::min(std::max(double(w.window), p0), p1);
+  const double m = std::min(std::max(double(w.window + w.sinks), p0), p1);
   n += (m * (m + 1) - p0 * (p0 + 1)) / 2;
-  n += (p1 - m) * double(std::min(w.window + w.sinks, w.sk));
+  n += (p1 - m) * double(w.window + w.sinks);
   return n * double(w.b) * w.heads;
 }
 
