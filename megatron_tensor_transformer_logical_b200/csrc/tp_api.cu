@@ -1450,7 +1450,7 @@ size_t tp_workspace_size(tp_op op, int64_t M, int64_t h, int64_t f, int heads, i
                          tp_dtype dtype) {
   try {
     if (op == TP_OP_QK_NORM_ROPE_BWD)  // also fp16
-      return (M > 0 && h > 0 && h <= 256 && dtype >= TP_F32 && dtype <= TP_F16) ? qk_rope_bwd_ws(h)
+      return (M >= 0 && h > 0 && h <= 256 && dtype >= TP_F32 && dtype <= TP_F16) ? qk_rope_bwd_ws(h)
                                                                                : 0;
     if (M <= 0 || h <= 0 || t < 1 || (dtype != TP_F32 && dtype != TP_BF16)) return 0;
     if (!dims_ok({M, h, f})) return 0;
