@@ -33,7 +33,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <cudaTypedefs.h>
 
 #include "attn_sm100.cuh"
 #include "ptx_sm100.cuh"
@@ -977,20 +976,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn_attn() {
-  // Initialised once, thread-safely (a function-local static).
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
-  return fn;
-}
-
 }  // namespace
 
 tp_status launch_attn_core_fwd_tc(const AttnShape& sh, const void* QKV, void* O, float* LSE,
@@ -998,7 +983,7 @@ tp_status launch_attn_core_fwd_tc(const AttnShape& sh, const void* QKV, void* O,
   if (sh.h / sh.heads != kD) return fail(TP_ERR_UNSUPPORTED, "attention: head dimension must be 128");
   if ((sh.s + kBM - 1) / kBM > 65535 || sh.b * sh.heads > 0x7fffffffLL)
     return fail(TP_ERR_SHAPE, "attention: sequence or b * heads too large");
-  auto fn = encode_fn_attn();
+  auto fn = tensor_map_encoder();
   if (fn == nullptr) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
   CUtensorMap map;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(3 * sh.h), static_cast<cuuint64_t>(sh.b * sh.s)};
@@ -1037,7 +1022,7 @@ tp_status launch_attn_core_fwd_tc(const AttnShape& sh, const void* QKV, void* O,
 
 namespace {
 bool make_map_f16(CUtensorMap* m, const void* ptr, int64_t cols, int64_t rows, int box_rows) {
-  auto fn = encode_fn_attn();
+  auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};

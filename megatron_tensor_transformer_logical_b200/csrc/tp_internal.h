@@ -1,6 +1,7 @@
 // Host-side interface between libtp's C entry points and its kernel launchers.
 #pragma once
 
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -27,6 +28,9 @@ int sm_count();
 // Unique id of the current CUDA context (cuCtxGetId), 0 if there is none or
 // it cannot be queried.  Caches of device-symbol addresses key on it.
 unsigned long long current_context_id();
+
+// The driver's cuTensorMapEncodeTiled, nullptr where it cannot be had.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // Launches a kernel.  With `after` it may be scheduled while the kernel before
 // it in the stream finishes; it then waits for that one itself (pdl_wait)

@@ -44,6 +44,7 @@
 #include <algorithm>
 
 #include "epi_math.cuh"
+#include "stream_mma.cuh"
 #include "tp_internal.h"
 
 namespace tp {
@@ -80,35 +81,6 @@ struct Cfg {
   static constexpr int kSum = 2 * MT * 16 * kCols * 4;       // both runs, K groups added
   static constexpr int kBytes = kRing > kRed + kSum ? kRing : kRed + kSum;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0 source bytes: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-
-template <bool TRANS>
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
-  if (TRANS)
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-  else
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
   float2 v;
@@ -225,8 +197,8 @@ __global__ void __launch_bounds__(kThreads, 2) thin_product(const ThinArgs a) {
       for (int e = 0; e < TERMS; ++e)
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          mma16816(acc[mt][2 * c], xf[e][mt], b[0], b[1]);
-          mma16816(acc[mt][2 * c + 1], xf[e][mt], b[2], b[3]);
+          mma16816<true>(acc[mt][2 * c], xf[e][mt], b[0], b[1]);
+          mma16816<true>(acc[mt][2 * c + 1], xf[e][mt], b[2], b[3]);
         }
     }
   }

@@ -45,7 +45,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cmath>
@@ -1469,24 +1468,11 @@ __global__ void __launch_bounds__(128) window_kv_join(const WinArgs a, int first
 
 // ------------------------------------------------------------------ host side
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn_win() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return static_cast<PFN_cuTensorMapEncodeTiled_v12000>(nullptr);
-  }();
-  return fn;
-}
-
 // [seqs][rows][cols] two-byte matrix with row stride ld (elements); boxes of
 // 64 columns x box_rows rows of one sequence, 128-byte swizzle.
 bool make_map3(CUtensorMap* m, const void* ptr, bool bf, int64_t cols, int64_t rows, int64_t seqs,
                int64_t ld, int box_rows) {
-  auto fn = encode_fn_win();
+  auto fn = tensor_map_encoder();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                         static_cast<cuuint64_t>(seqs)};
