@@ -523,7 +523,8 @@ tp_status tp_qk_norm_rope_bwd(const void* Q, int64_t ldq, const void* K, int64_t
  *   are fp32.
  * What a query does not see is multiplied by a probability of zero inside its
  * tile, so every Q, K and V (and dO) value of its own sequence must be finite;
- * other sequences never enter.
+ * other sequences never enter.  A NaN score makes O and LSE of the queries that
+ * see it NaN, never the 0 and -inf of a query that sees nothing.
  * Errors: NULL; sizes, heads % kv_heads, strides (TP_ERR_SHAPE); window < 1,
  *   sinks < 0, scale < 0 or not finite (TP_ERR_SHAPE); alignment; dtype; d
  *   other than 64 or 128 (TP_ERR_UNSUPPORTED).

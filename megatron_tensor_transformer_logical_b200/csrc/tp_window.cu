@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && total > 0) ok = wait_o(last);
       if (!ok) break;
       g0 += static_cast<uint32_t>(bl.n);
-      const bool some = l_run > 0.0f;
+      const bool some = l_run != 0.0f;  // also when it is NaN, and O then is
       const float inv = some ? 1.0f / l_run : 0.0f;
 #pragma unroll 1
       for (int h = 0; h < DH / 64; ++h) {

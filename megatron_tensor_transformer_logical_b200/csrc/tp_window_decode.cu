@@ -22,7 +22,8 @@
 // term and the empty rows computed 87.4).  Larger groups take a second one (16
 // such sequences, groups of 16: 69.2 against 65.0 us with one term).
 // Keys past the visible range are read as zeros and masked, so what the
-// cache holds beyond lens never enters, whatever it is.
+// cache holds beyond lens never enters, whatever it is.  A sum of 0 stands for
+// no key at all; the sum of a row with a NaN score is NaN, and so is its O.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -318,7 +319,7 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 ml = sml[w * kRows + r];
-      if (ml.x == -INFINITY) continue;  // this warp saw no key
+      if (ml.y == 0.0f) continue;  // this warp saw no key
       const float f = ex2_approx(ml.x - mm);
       acc = fmaf(f, so[(w * kRows + r) * DH + c], acc);
       ll = fmaf(f, ml.y, ll);
@@ -328,10 +329,10 @@ __global__ void __launch_bounds__(kThreads) window_decode(const DecArgs a) {
       a.po[p * DH + c] = acc;
       if (c == 0) a.pml[p] = make_float2(mm, ll);
     } else {
-      store1<BF>(a.o, bi * a.ldo + (head0 + r) * DH + c, ll > 0.0f ? acc / ll : 0.0f);
+      store1<BF>(a.o, bi * a.ldo + (head0 + r) * DH + c, ll != 0.0f ? acc / ll : 0.0f);
       if (c == 0 && a.lse != nullptr)
         a.lse[static_cast<long long>(bi) * a.heads + head0 + r] =
-            ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
     }
   }
 }
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
 #pragma unroll
   for (int w = 0; w < 8; ++w) mm = fmaxf(mm, s_red[w]);
   __syncthreads();
-  const float wgt = ml.x == -INFINITY ? 0.0f : ex2_approx(ml.x - mm);
+  const float wgt = ml.y == 0.0f ? 0.0f : ex2_approx(ml.x - mm);
   if (static_cast<int>(threadIdx.x) < a.splits) s_w[threadIdx.x] = wgt;
   float ll = wgt * ml.y;
 #pragma unroll
@@ -395,14 +396,14 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
       acc.z += v.z;
       acc.w += v.w;
     }
-    const float inv = ll > 0.0f ? 1.0f / ll : 0.0f;
+    const float inv = ll != 0.0f ? 1.0f / ll : 0.0f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + bi * a.ldo +
                                                 head * DH + 4 * c);
     dst[0] = pack2<BF>(acc.x * inv, acc.y * inv);
     dst[1] = pack2<BF>(acc.z * inv, acc.w * inv);
     if (c == 0 && a.lse != nullptr)
       a.lse[static_cast<long long>(bi) * a.heads + head] =
-          ll > 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+          ll != 0.0f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
   }
 }
 
