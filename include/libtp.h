@@ -540,6 +540,9 @@ tp_status tp_window_attn_fwd(const void* Q, int64_t ldq, const void* K, int64_t 
  *   dQ = scale dS K,  dK = scale dS^T Q,  dV = P^T dO,
  * dK and dV summed over the query heads that share them.  Every row of dQ,
  * dK and dV is written (zeros where nothing is seen).  Deterministic.
+ *   P and dS are rounded to dtype for their products.  With TP_F16 a dS past
+ *   65504 makes the gradients it enters infinite or NaN, and one below 2^-25
+ *   vanishes, as values of an fp16 dO would: scale the loss for both.
  *   O, LSE: from the forward, same arguments.  No output overlaps an input.
  *   ws: tp_window_attn_workspace_size() bytes.
  * Errors: as the forward, plus TP_ERR_WORKSPACE.
