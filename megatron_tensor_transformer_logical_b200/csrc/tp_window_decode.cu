@@ -407,22 +407,19 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
   }
 }
 
-// Slices per (sequence, key head): as many as run at once (two blocks per SM),
-// each at least kMinKeys keys.  One round of long slices beats several rounds of
-// short ones, and a last round of few blocks: one sequence of 131072 keys, 4 key
-// heads of 128 in bf16 (267 MB), 48 us with 74 slices, 56 with 148, 70 with 255;
-// 8, 20, 24, 32 and 36 sequences of 4100 visible keys, 8 key heads (537 MB for
-// 32), 26, 62, 64, 79 and 90 us so and 34, 70, 79, 85 and 95 us with a slice
-// more.  All sequences get the same number, whatever their lengths; from 2 SMs
-// of items on they are not cut, and what is left after whole rounds shows (38
-// sequences, 304 items: 126 us).
+// Slices per (sequence, key head): as many as fill the blocks that run at once
+// (two per SM), each at least kMinKeys keys.  One round of long slices beats
+// several rounds of short ones: one sequence of 131072 keys, 4 key heads of
+// 128 in bf16 (267 MB), 48 us with 74 slices, 56 with 148, 70 with 255; 32
+// sequences of 4100 visible keys, 8 key heads (537 MB): 87 us with two slices,
+// 91 with four, 96 with five.
 constexpr int kMinKeys = 256;
 
 int plan_splits(const WindowDecode& w) {
   const int64_t gt = (w.heads / w.kv_heads + kRows - 1) / kRows;
   const int64_t items = w.b * w.kv_heads * gt;
   const int64_t keys = std::min(w.cap, w.window + w.sinks);
-  const int64_t want = 2LL * sm_count() / items;
+  const int64_t want = (2LL * sm_count() + items - 1) / items;
   return static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>({want, (keys + kMinKeys - 1) / kMinKeys, kMaxSplits})));
 }
@@ -478,8 +475,8 @@ tp_status decode(const WindowDecode& w, void* scratch, cudaStream_t stream) {
 
 }  // namespace
 
-// Enough for this batch and every smaller one: n items are cut into at most 2
-// SMs slices in all, so fewer than 2 SMs + n, which grows with the batch.
+// Enough for this batch and every smaller one: n items are cut into fewer than
+// 2 SMs + n slices, and into none from 2 SMs on.
 size_t window_decode_scratch_bytes(const WindowDecode& w) {
   const int64_t keys = std::min(w.cap, w.window + w.sinks);
   const int64_t most = std::min<int64_t>((keys + kMinKeys - 1) / kMinKeys, kMaxSplits);

@@ -114,21 +114,3 @@ def test_a_sequence_does_not_depend_on_its_batch():
     for i in (2, 4, 5):
         one, _ = call(Q[i:i + 1], K[i:i + 1], V[i:i + 1], lens[i:i + 1], heads, kv, window, 0)
         close(one, ref[i:i + 1], tO[i:i + 1], f"alone {i}")
-
-
-@pytest.mark.parametrize("b,kv,cap", [(1, 1, 200), (1, 2, 3000), (18, 8, 600), (20, 8, 600),
-                                      (36, 8, 600), (38, 8, 600)])
-def test_slices_run_in_one_round(b, kv, cap):
-    """A sequence is cut only while all slices run at once, two per SM: at more
-    than an SM of items each is one block, and no second kernel joins it."""
-    d, items = 64, b * kv
-    sms = torch.cuda.get_device_properties(0).multi_processor_count
-    lens = lengths(b, cap)
-    Q, K, V = make(b, cap, 2 * kv, kv, d, BF, lens, 4)
-    call(Q, K, V, lens, 2 * kv, kv, cap, 0)
-    before = L.tp_launch_count()
-    O, _ = call(Q, K, V, lens, 2 * kv, kv, cap, 0)
-    cut = min(2 * sms // items, -(-cap // 256)) > 1
-    assert L.tp_launch_count() - before == (2 if cut else 1)
-    ref, tO, _, _ = reference(Q, K, V, lens, 2 * kv, kv, cap, 0)
-    close(O, ref, tO, "O")
