@@ -40,7 +40,9 @@
 // already costs as much accuracy as the results' own rounding, and the
 // rounding of dS would come on top (gradients 1.5-1.8 times as far from exact
 // as their rounding alone, 1.1-1.4 times with the two terms).  Rows with many
-// keys average both out.
+// keys average the error of D out; the one rounding of P and of dS stays, and
+// O and the gradients are 1.3 times as far off as their own rounding (2.1e-3
+// against 1.6e-3 in bf16).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -349,11 +351,14 @@ struct FwdItem {
 // previous item's last S is done, and the next item's first two S run under an
 // item's epilogue (a launch, load and epilogue of its own took 19% of an
 // item of 20 blocks).
-// Bound by the tensor pipe: a tile's block of 64 keys takes it 384 clocks for S
-// (both operands from shared memory, 6 KB per product of 32 clocks) and 256
-// for P V, 1280 for both tiles, and a pair of blocks takes 1550.  Measured:
-// 8192 tokens, 32 heads of 128, window 1024, 4 sinks (129 GFLOP) 160 us, 806
-// TFLOP/s; tensor pipe 47% of the cycles, exponentials 42%.
+// What bounds it is the tensor pipe in the shape chosen here, not at its rate:
+// with N = 64 and both operands in shared memory a product of 32 clocks holds
+// the pipe for 48 (6 KB of operands), so a tile's block of 64 keys takes it 384
+// clocks for S and 256 for P V, 1280 for both tiles, and a pair of blocks takes
+// 1550.  Measured: 8192 tokens, 32 heads of 128, window 1024, 4 sinks (129
+// GFLOP) 159 us, 810 TFLOP/s (through the Python call, one at a time, 181);
+// tensor pipe active in 47% of the cycles, which is 80% of what that shape
+// allows; exponentials 42%.
 template <bool BF, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     window_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

@@ -18,8 +18,8 @@
 // own rounding alone (with one term 1.4 times that), whatever else is in the
 // batch.  Groups of up to 8 query heads leave the rows 8-15 of the product
 // empty: the rests go there and cost no product of their own (32 sequences of
-// 4100 visible keys, 8 key heads of 128 read by 4 heads each: 85.6 us; with one
-// term and the empty rows computed 87.4).  Larger groups take a second one (16
+// 4100 visible keys, 8 key heads of 128 read by 4 heads each, in two slices: 85.0
+// us; with one term and the empty rows computed 86.9).  Larger groups take a second one (16
 // such sequences, groups of 16: 69.2 against 65.0 us with one term).
 // Keys past the visible range are read as zeros and masked, so what the
 // cache holds beyond lens never enters, whatever it is.  A sum of 0 stands for
@@ -408,11 +408,15 @@ __global__ void __launch_bounds__(256) window_decode_join(const DecArgs a) {
 }
 
 // Slices per (sequence, key head): as many as fill the blocks that run at once
-// (two per SM), each at least kMinKeys keys.  One round of long slices beats
-// several rounds of short ones: one sequence of 131072 keys, 4 key heads of
-// 128 in bf16 (267 MB), 48 us with 74 slices, 56 with 148, 70 with 255; 32
-// sequences of 4100 visible keys, 8 key heads (537 MB): 87 us with two slices,
-// 91 with four, 96 with five.
+// (two per SM), rounded up, each at least kMinKeys keys; from 2 SMs of items on
+// none is cut.  More and shorter ones cost more joining: one sequence of 131072
+// keys, 4 key heads of 128 in bf16 (267 MB), 48 us with 74 slices, 56 with 148,
+// 70 with 255; 32 sequences of 4100 visible keys, 8 key heads (537 MB): 85 us
+// with two, 91 with four, 96 with five.  Rounding up starts a second round of
+// blocks, which costs sequences of one length (20 and 32 of 4100 keys: 70 and 85
+// us, rounded down 62 and 79) and gains more where lengths differ, since all get
+// the same number of slices (20 of 1 to 8192 keys: 59 us, rounded down 95; one of
+// 65536 keys among 31 of 512: 324 against 621, where the bytes alone take 51).
 constexpr int kMinKeys = 256;
 
 int plan_splits(const WindowDecode& w) {
